@@ -260,13 +260,14 @@ __device__ __forceinline__ float block_top(const float (&x)[8])
 // Up to the next e4m3 code with the chance of the remainder: adding 20 random
 // bits below the three kept mantissa bits and cutting them off.  Below 2^-6 the
 // codes are evenly spaced; 2^-6 more puts them into the binade of that spacing.
-// What is above 0 becomes code 1 (2^-9) at least; NaN stays.
+// What is above 0 becomes code 1 (2^-9) at least; NaN, which the random bits would carry into a zero,
+// stays (45 M elements, in a graph: 126.9 us; 125.7 without that, 129.6 where a maximum of the block's looks for it).
 __device__ __forceinline__ float stochastic_e4m3(float y, uint32_t rnd20)
 {
     y = fmaxf(y, y > 0.0f ? 0x1p-9f : y);
     const float lift = y < 0x1p-6f ? 0x1p-6f : 0.0f;
     const float z = __uint_as_float((__float_as_uint(__fadd_rn(y, lift)) + rnd20) & 0xfff00000u) - lift;
-    return z > kE4m3Max ? kE4m3Max : z;
+    return y == y ? fminf(z, kE4m3Max) : y;
 }
 
 // a / b within two units of the last place: the update is a small part of p, whose own rounding
