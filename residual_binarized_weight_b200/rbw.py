@@ -7,6 +7,7 @@ issued on torch's current stream.  A missing library raises immediately
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -144,6 +145,23 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on(stream):
+    """Where a call on `stream` allocates: in that stream's memory if one is given, so that what the call makes for itself
+    is not given out again before the call has run."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream=None):
+    """A result of a call on `stream`, kept until the current stream, which may read it, is done with it as well."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if t.is_cuda:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def packed_words(n_out, k_in, k_planes):
     return int(lib().rb_packed_words(n_out, k_in, k_planes))
 
@@ -151,17 +169,17 @@ def packed_words(n_out, k_in, k_planes):
 class PackedLayer:
     """Device tensors of one packed layer (owns them) plus its rb_layer_t view."""
 
-    def __init__(self, n_out, k_in, k_planes, device="cuda", g16=None, h16=None, planes=None):
-        """New planes and scale tensors unless existing ones are passed to share."""
+    def __init__(self, n_out, k_in, k_planes, device="cuda", g16=None, h16=None, planes=None, stream=None):
+        """New planes and scale tensors (for use on `stream`) unless existing ones are passed to share."""
         nw = packed_words(n_out, k_in, k_planes)
         if nw == 0:
             raise ValueError("invalid layer shape")
         self.n_out, self.k_in, self.k_planes = n_out, k_in, k_planes
-        self.planes = torch.empty(nw, dtype=torch.int32, device=device) if planes is None else planes
+        self.planes = _empty(nw, torch.int32, device, stream) if planes is None else planes
         if self.planes.numel() != nw or self.planes.element_size() != 4 or not self.planes.is_contiguous():
             raise ValueError("planes do not match the layer shape")
-        self.g16 = torch.empty(k_planes, n_out, dtype=torch.float16, device=device) if g16 is None else g16
-        self.h16 = torch.empty(k_planes, k_in, dtype=torch.float16, device=device) if h16 is None else h16
+        self.g16 = _empty((k_planes, n_out), torch.float16, device, stream) if g16 is None else g16
+        self.h16 = _empty((k_planes, k_in), torch.float16, device, stream) if h16 is None else h16
         if tuple(self.g16.shape) != (k_planes, n_out) or tuple(self.h16.shape) != (k_planes, k_in):
             raise ValueError("scale tensors do not match the layer shape")
 
@@ -176,7 +194,7 @@ class PackedLayer:
 def pack(W, g, h, k_planes, out: PackedLayer | None = None, dev_status=None, stream=None):
     """rb_pack: W fp32 [N][K], g fp32 [k][N], h fp32 [k][K] (CUDA) -> PackedLayer."""
     N, K = W.shape
-    out = out or PackedLayer(N, K, k_planes, W.device)
+    out = out or PackedLayer(N, K, k_planes, W.device, stream=stream)
     st = lib().rb_pack(_ptr(W), _ptr(g), _ptr(h), N, K, k_planes, _ptr(out.planes), _ptr(out.g16),
                        _ptr(out.h16), _ptr(dev_status), _stream(stream))
     _check("rb_pack", st)
@@ -195,9 +213,10 @@ def svid_workspace_bytes(n_out, k_in):
     return int(lib().rb_svid_workspace_bytes(n_out, k_in))
 
 
-def workspace(nbytes, device="cuda"):
-    """Zero-filled device workspace (uint8) of at least nbytes (16-byte aligned)."""
-    return torch.zeros(max(int(nbytes), 16), dtype=torch.uint8, device=device)
+def workspace(nbytes, device="cuda", stream=None):
+    """Zero-filled device workspace (uint8) of at least nbytes (16-byte aligned), for a call on `stream`."""
+    with _on(stream):
+        return torch.zeros(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
 def _apply(fn_name, layer: PackedLayer, X, Y, ws, flags, dev_status, stream):
@@ -214,7 +233,7 @@ def _apply(fn_name, layer: PackedLayer, X, Y, ws, flags, dev_status, stream):
 def gemv(layer: PackedLayer, X, Y=None, ws=None, flags=0, dev_status=None, stream=None, y_dtype=torch.float32):
     """rb_gemv: X bf16 [M][K] (M <= 64) -> Y [M][N] (fp32 or bf16)."""
     if Y is None:
-        Y = torch.empty(X.shape[0], layer.n_out, dtype=y_dtype, device=X.device)
+        Y = _empty((X.shape[0], layer.n_out), y_dtype, X.device, stream)
     return _apply("rb_gemv", layer, X, Y, ws, flags, dev_status, stream)
 
 
@@ -236,7 +255,7 @@ def gemv_batch(layers, Xs, Ys, flags=0, dev_status=None, stream=None):
 def gemm(layer: PackedLayer, X, Y=None, ws=None, flags=0, dev_status=None, stream=None, y_dtype=torch.float32):
     """rb_gemm: X bf16 [M][K] -> Y [M][N] (fp32 or bf16) on the tcgen05 tensor cores."""
     if Y is None:
-        Y = torch.empty(X.shape[0], layer.n_out, dtype=y_dtype, device=X.device)
+        Y = _empty((X.shape[0], layer.n_out), y_dtype, X.device, stream)
     return _apply("rb_gemm", layer, X, Y, ws, flags, dev_status, stream)
 
 
@@ -244,7 +263,7 @@ def gemm_wait_limit(layer: PackedLayer, X, wait_limit_ns, Y=None, ws=None, flags
                     y_dtype=torch.float32):
     """rb_gemm_wait_limit: rb_gemm with a caller-chosen bound (ns) on every device-side wait."""
     if Y is None:
-        Y = torch.empty(X.shape[0], layer.n_out, dtype=y_dtype, device=X.device)
+        Y = _empty((X.shape[0], layer.n_out), y_dtype, X.device, stream)
     L = layer.struct()
     ydt = RB_BF16 if Y.dtype == torch.bfloat16 else RB_F32
     wsp, wsb = (None, 0) if ws is None else (_ptr(ws), ws.numel() * ws.element_size())
@@ -257,7 +276,7 @@ def gemm_wait_limit(layer: PackedLayer, X, wait_limit_ns, Y=None, ws=None, flags
 def gemm_noalloc(layer: PackedLayer, X, Y=None, flags=0, dev_status=None, stream=None, y_dtype=torch.float32):
     """rb_gemm_noalloc: rb_gemm without a workspace (fixed 32 MiB library scratch; see include/rbw.h)."""
     if Y is None:
-        Y = torch.empty(X.shape[0], layer.n_out, dtype=y_dtype, device=X.device)
+        Y = _empty((X.shape[0], layer.n_out), y_dtype, X.device, stream)
     L = layer.struct()
     ydt = RB_BF16 if Y.dtype == torch.bfloat16 else RB_F32
     st = lib().rb_gemm_noalloc(ctypes.byref(L), _ptr(X), X.shape[0], _ptr(Y), ydt, _ptr(dev_status), flags,
@@ -271,7 +290,8 @@ def transpose(layer: PackedLayer, out: PackedLayer | None = None, stream=None):
     scale tensors are shared with `layer`, exchanged).  Its forward product is
     the input gradient: gemv/gemm(transpose(layer), dY) = dY . What."""
     if out is None:
-        out = PackedLayer(layer.k_in, layer.n_out, layer.k_planes, layer.planes.device, g16=layer.h16, h16=layer.g16)
+        out = PackedLayer(layer.k_in, layer.n_out, layer.k_planes, layer.planes.device, g16=layer.h16, h16=layer.g16,
+                          stream=stream)
     elif (out.n_out, out.k_in, out.k_planes) != (layer.k_in, layer.n_out, layer.k_planes):
         raise ValueError("out is not shaped as the transposed layer")
     else:
@@ -289,7 +309,7 @@ def rowmajor_words(n_out, k_in, k_planes):
 def planes_from_rowmajor(rowmajor, n_out, k_in, k_planes, out: PackedLayer | None = None, stream=None):
     """rb_planes_from_rowmajor: plain [k][N][K/32] LSB-first words (int32 CUDA tensor)
     -> a PackedLayer whose planes hold them in the storage layout (scales left to the caller)."""
-    out = out or PackedLayer(n_out, k_in, k_planes, rowmajor.device)
+    out = out or PackedLayer(n_out, k_in, k_planes, rowmajor.device, stream=stream)
     st = lib().rb_planes_from_rowmajor(_ptr(rowmajor), n_out, k_in, k_planes, _ptr(out.planes), _stream(stream))
     _check("rb_planes_from_rowmajor", st)
     return out
@@ -298,7 +318,7 @@ def planes_from_rowmajor(rowmajor, n_out, k_in, k_planes, out: PackedLayer | Non
 def planes_to_rowmajor(layer: PackedLayer, out=None, stream=None):
     """rb_planes_to_rowmajor: the layer's planes as plain [k][N][K/32] LSB-first words (int32)."""
     n = rowmajor_words(layer.n_out, layer.k_in, layer.k_planes)
-    out = out if out is not None else torch.empty(n, dtype=torch.int32, device=layer.planes.device)
+    out = out if out is not None else _empty(n, torch.int32, layer.planes.device, stream)
     st = lib().rb_planes_to_rowmajor(_ptr(layer.planes), layer.n_out, layer.k_in, layer.k_planes, _ptr(out),
                                      _stream(stream))
     _check("rb_planes_to_rowmajor", st)
@@ -315,8 +335,8 @@ def qat_forward(W, g, h, k_planes, X, Y=None, ws=None, flags=0, dev_status=None,
     N, K = W.shape
     M = X.shape[0]
     if Y is None:
-        Y = torch.empty(M, N, dtype=y_dtype, device=W.device)
-    ws = ws if ws is not None else workspace(qat_forward_workspace_bytes(N, K, k_planes, M), W.device)
+        Y = _empty((M, N), y_dtype, W.device, stream)
+    ws = ws if ws is not None else workspace(qat_forward_workspace_bytes(N, K, k_planes, M), W.device, stream)
     ydt = RB_BF16 if Y.dtype == torch.bfloat16 else RB_F32
     st = lib().rb_qat_forward(_ptr(W), _ptr(g), _ptr(h), N, K, k_planes, _ptr(X), M, _ptr(Y), ydt, _ptr(ws),
                               ws.numel(), _ptr(dev_status), flags, _stream(stream))
@@ -330,11 +350,11 @@ def qat_backward(layer: PackedLayer, g, h, X, dY, dW=None, dg=None, dh=None, ws=
     g [k][N], h [k][K], X bf16 [M][K] and dY bf16 [M][N] (CUDA tensors)."""
     N, K, k = layer.n_out, layer.k_in, layer.k_planes
     dev = layer.planes.device
-    dW = dW if dW is not None else torch.empty(N, K, dtype=torch.float32, device=dev)
-    dg = dg if dg is not None else torch.empty(k, N, dtype=torch.float32, device=dev)
-    dh = dh if dh is not None else torch.empty(k, K, dtype=torch.float32, device=dev)
+    dW = dW if dW is not None else _empty((N, K), torch.float32, dev, stream)
+    dg = dg if dg is not None else _empty((k, N), torch.float32, dev, stream)
+    dh = dh if dh is not None else _empty((k, K), torch.float32, dev, stream)
     nb = int(lib().rb_qat_backward_workspace_bytes(N, K, k))
-    ws = ws if ws is not None else workspace(nb, dev)
+    ws = ws if ws is not None else workspace(nb, dev, stream)
     st = lib().rb_qat_backward(_ptr(layer.planes), _ptr(g), _ptr(h), N, K, k, _ptr(X), _ptr(dY), X.shape[0],
                                _ptr(dW), _ptr(dg), _ptr(dh), _ptr(ws), ws.numel(), _ptr(dev_status), _stream(stream))
     _check("rb_qat_backward", st)
@@ -344,9 +364,9 @@ def qat_backward(layer: PackedLayer, g, h, X, dY, dW=None, dg=None, dh=None, ws=
 def svid_greedy(W, k_planes, iters=20, ws=None, stream=None):
     """rb_svid_greedy: fp32 W [N][K] (CUDA) -> (g [k][N], h [k][K]) fp32."""
     N, K = W.shape
-    g = torch.empty(k_planes, N, dtype=torch.float32, device=W.device)
-    h = torch.empty(k_planes, K, dtype=torch.float32, device=W.device)
-    ws = ws if ws is not None else workspace(svid_workspace_bytes(N, K), W.device)
+    g = _empty((k_planes, N), torch.float32, W.device, stream)
+    h = _empty((k_planes, K), torch.float32, W.device, stream)
+    ws = ws if ws is not None else workspace(svid_workspace_bytes(N, K), W.device, stream)
     st = lib().rb_svid_greedy(_ptr(W), N, K, k_planes, iters, _ptr(g), _ptr(h), _ptr(ws),
                               ws.numel(), _stream(stream))
     _check("rb_svid_greedy", st)
@@ -356,10 +376,10 @@ def svid_greedy(W, k_planes, iters=20, ws=None, stream=None):
 def svid_iterative(W, k_planes, sweeps=20, iters=20, ws=None, stream=None):
     """rb_svid_iterative: greedy scales refined by Gauss-Seidel sweeps; fp32 W [N][K] (CUDA)."""
     N, K = W.shape
-    g = torch.empty(k_planes, N, dtype=torch.float32, device=W.device)
-    h = torch.empty(k_planes, K, dtype=torch.float32, device=W.device)
+    g = _empty((k_planes, N), torch.float32, W.device, stream)
+    h = _empty((k_planes, K), torch.float32, W.device, stream)
     nbytes = int(lib().rb_svid_iterative_workspace_bytes(N, K, k_planes))
-    ws = ws if ws is not None else workspace(nbytes, W.device)
+    ws = ws if ws is not None else workspace(nbytes, W.device, stream)
     st = lib().rb_svid_iterative(_ptr(W), N, K, k_planes, sweeps, iters, _ptr(g), _ptr(h), _ptr(ws),
                                  ws.numel(), _stream(stream))
     _check("rb_svid_iterative", st)
@@ -371,11 +391,11 @@ def svid_pack(W, k_planes, sweeps=0, iters=20, out: PackedLayer | None = None, w
     """rb_svid_pack: fp32 W [N][K] (CUDA) -> (PackedLayer, g, h): SVID scales (greedy when sweeps = 0,
     else iterative) and the packed planes, in one device-side call."""
     N, K = W.shape
-    out = out or PackedLayer(N, K, k_planes, W.device)
-    g = torch.empty(k_planes, N, dtype=torch.float32, device=W.device)
-    h = torch.empty(k_planes, K, dtype=torch.float32, device=W.device)
+    out = out or PackedLayer(N, K, k_planes, W.device, stream=stream)
+    g = _empty((k_planes, N), torch.float32, W.device, stream)
+    h = _empty((k_planes, K), torch.float32, W.device, stream)
     nbytes = int(lib().rb_svid_pack_workspace_bytes(N, K, k_planes))
-    ws = ws if ws is not None else workspace(nbytes, W.device)
+    ws = ws if ws is not None else workspace(nbytes, W.device, stream)
     st = lib().rb_svid_pack(_ptr(W), N, K, k_planes, sweeps, iters, _ptr(g), _ptr(h), _ptr(out.planes),
                             _ptr(out.g16), _ptr(out.h16), _ptr(ws), ws.numel(), _ptr(dev_status), _stream(stream))
     _check("rb_svid_pack", st)
@@ -392,7 +412,7 @@ def shard_bounds(n_out, world, rank):
 
 def shard_rows(layer: PackedLayer, row0, rows, stream=None):
     """rb_shard_rows: rows [row0, row0 + rows) of `layer` as a PackedLayer sharing its h16."""
-    out = PackedLayer(rows, layer.k_in, layer.k_planes, layer.planes.device, h16=layer.h16)
+    out = PackedLayer(rows, layer.k_in, layer.k_planes, layer.planes.device, h16=layer.h16, stream=stream)
     L = layer.struct()
     st = lib().rb_shard_rows(ctypes.byref(L), row0, rows, _ptr(out.planes), _ptr(out.g16), _stream(stream))
     _check("rb_shard_rows", st)
@@ -403,15 +423,16 @@ def shard_rows(layer: PackedLayer, row0, rows, stream=None):
 class BtcLayer:
     """Device tensors of a binary-codebook layer (owns the codebooks and index streams; shares g16, h16)."""
 
-    def __init__(self, n_out, k_in, k_planes, c_max, g16, h16, device="cuda"):
+    def __init__(self, n_out, k_in, k_planes, c_max, g16, h16, device="cuda", stream=None):
         self.n_out, self.k_in, self.k_planes, self.c_max = n_out, k_in, k_planes, c_max
         self.index_bits = int(lib().rb_btc_index_bits(c_max))
         self.row_words = int(lib().rb_btc_row_words(k_in, self.index_bits))
         if self.index_bits == 0 or self.row_words == 0:
             raise ValueError("invalid codebook layer shape")
-        self.codebooks = torch.zeros(k_planes, c_max, dtype=torch.int16, device=device)
-        self.indices = torch.zeros(k_planes, n_out, self.row_words, dtype=torch.int32, device=device)
-        self.sizes = torch.zeros(k_planes, 4, dtype=torch.int32, device=device)   # c of each plane in column 0
+        with _on(stream):
+            self.codebooks = torch.zeros(k_planes, c_max, dtype=torch.int16, device=device)
+            self.indices = torch.zeros(k_planes, n_out, self.row_words, dtype=torch.int32, device=device)
+            self.sizes = torch.zeros(k_planes, 4, dtype=torch.int32, device=device)   # c of each plane in column 0
         self.g16, self.h16 = g16, h16
 
     def struct(self):
@@ -425,8 +446,8 @@ class BtcLayer:
 
 def btc_encode(layer: PackedLayer, c_max, iters=10, stream=None):
     """rb_btc_encode for every plane of a packed layer -> BtcLayer."""
-    out = BtcLayer(layer.n_out, layer.k_in, layer.k_planes, c_max, layer.g16, layer.h16, layer.planes.device)
-    ws = workspace(int(lib().rb_btc_encode_workspace_bytes(c_max)), layer.planes.device)
+    out = BtcLayer(layer.n_out, layer.k_in, layer.k_planes, c_max, layer.g16, layer.h16, layer.planes.device, stream)
+    ws = workspace(int(lib().rb_btc_encode_workspace_bytes(c_max)), layer.planes.device, stream)
     L = layer.struct()
     for i in range(layer.k_planes):
         st = lib().rb_btc_encode(ctypes.byref(L), i, c_max, iters, _ptr(out.codebooks[i]), _ptr(out.sizes[i]),
@@ -438,9 +459,9 @@ def btc_encode(layer: PackedLayer, c_max, iters=10, stream=None):
 def btc_gemv(layer: BtcLayer, X, Y=None, ws=None, flags=0, stream=None, y_dtype=torch.float32):
     """rb_btc_gemv: X bf16 [1][K] (or [K]) -> Y [1][N]."""
     if Y is None:
-        Y = torch.empty(1, layer.n_out, dtype=y_dtype, device=X.device)
+        Y = _empty((1, layer.n_out), y_dtype, X.device, stream)
     ws = ws if ws is not None else workspace(int(lib().rb_btc_gemv_workspace_bytes(layer.n_out, layer.k_in)),
-                                             X.device)
+                                             X.device, stream)
     L = layer.struct()
     ydt = RB_BF16 if Y.dtype == torch.bfloat16 else RB_F32
     st = lib().rb_btc_gemv(ctypes.byref(L), _ptr(X), _ptr(Y), ydt, _ptr(ws), ws.numel(), None, flags,
@@ -458,7 +479,7 @@ def btc_gemv_batch(layers, Xs, Ys, ws=None, flags=0, stream=None):
     yp = (ctypes.c_void_p * n)(*[Y.data_ptr() for Y in Ys])
     L0 = layers[0]
     ws = ws if ws is not None else workspace(
-        int(lib().rb_btc_gemv_batch_workspace_bytes(L0.n_out, L0.k_in, n)), Xs[0].device)
+        int(lib().rb_btc_gemv_batch_workspace_bytes(L0.n_out, L0.k_in, n)), Xs[0].device, stream)
     ydt = RB_BF16 if Ys[0].dtype == torch.bfloat16 else RB_F32
     st = lib().rb_btc_gemv_batch(lp, xp, yp, n, ydt, _ptr(ws), ws.numel(), None, flags, _stream(stream))
     _check("rb_btc_gemv_batch", st)
@@ -466,6 +487,14 @@ def btc_gemv_batch(layers, Xs, Ys, ws=None, flags=0, stream=None):
 
 
 # ---------------------------------------------------------------- epilogue gradient
+def _scratch(nbytes, device, stream):
+    """A call's own workspace, not cleared."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with _on(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 _BF16 = (torch.bfloat16,)
 
 
@@ -531,12 +560,12 @@ def linear(layer: PackedLayer, X, Y=None, bias=None, act="none", mul=None, resid
     M, N, K = X.shape[0], layer.n_out, layer.k_in
     dev, st = _current(stream)
     if Y is None:
-        Y = torch.empty((M, N), dtype=y_dtype, device=X.device)
+        Y = _empty((M, N), y_dtype, X.device, stream)
     xp, ldx = _matrix(X, "X", M, K, dev)
     yp, ldy = _matrix(Y, "Y", M, N, dev, _Y_TYPES)
     E = _epilogue(M, N, dev, bias, act, mul, residual, preact)
     if ws is None:
-        ws = torch.empty(linear_workspace_bytes(N, K, layer.k_planes, M), dtype=torch.uint8, device=X.device)
+        ws = _scratch(linear_workspace_bytes(N, K, layer.k_planes, M), X.device, stream)
     if not layer.planes.get_device() == layer.g16.get_device() == layer.h16.get_device() == ws.get_device() == dev:
         raise ValueError("layer and ws: expected tensors on the current CUDA device")
     st = lib().rb_linear(ctypes.byref(layer.struct()), xp, ldx, M, ctypes.byref(E), yp, ldy,
@@ -557,13 +586,13 @@ def qat_linear(W, g, h, k_planes, X, Y=None, bias=None, act="none", mul=None, re
     N, K = W.shape
     M = X.shape[0]
     if Y is None:
-        Y = torch.empty(M, N, dtype=y_dtype, device=X.device)
+        Y = _empty((M, N), y_dtype, X.device, stream)
     dev, st = _current(stream)
     xp, ldx = _matrix(X, "X", M, K, dev)
     yp, ldy = _matrix(Y, "Y", M, N, dev, _Y_TYPES)
     E = _epilogue(M, N, dev, bias, act, mul, residual, preact)
     if ws is None:
-        ws = torch.empty(qat_linear_workspace_bytes(N, K, k_planes, M), dtype=torch.uint8, device=X.device)
+        ws = _scratch(qat_linear_workspace_bytes(N, K, k_planes, M), X.device, stream)
     if ws.get_device() != dev:
         raise ValueError("ws: expected a tensor on the current CUDA device")
     st = lib().rb_qat_linear(_vector(W, "W", N * K, dev), _vector(g, "g", k_planes * N, dev),
@@ -584,16 +613,16 @@ def epilogue_backward(dY, preact, act="none", mul=None, bias=True, dP=None, dmul
     may be strided).  dmul is None without mul, dbias (fp32 [N]) without bias; the residual's gradient is dY."""
     M, N = dY.shape
     if dP is None:
-        dP = torch.empty((M, N), dtype=torch.bfloat16, device=dY.device)
+        dP = _empty((M, N), torch.bfloat16, dY.device, stream)
     if dmul is None and mul is not None:
-        dmul = torch.empty((M, N), dtype=torch.bfloat16, device=dY.device)
+        dmul = _empty((M, N), torch.bfloat16, dY.device, stream)
     if dbias is None and bias:
-        dbias = torch.empty(N, dtype=torch.float32, device=dY.device)
+        dbias = _empty(N, torch.float32, dY.device, stream)
     dev, st = _current(stream)
     wsp, wsb = None, 0
     if dbias is not None:
         if ws is None:
-            ws = torch.empty(epilogue_backward_workspace_bytes(M, N), dtype=torch.uint8, device=dY.device)
+            ws = _scratch(epilogue_backward_workspace_bytes(M, N), dY.device, stream)
         if ws.get_device() != dev:
             raise ValueError("ws: expected a tensor on the current CUDA device")
         wsp, wsb = ws.data_ptr(), ws.nbytes

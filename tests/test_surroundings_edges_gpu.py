@@ -1,10 +1,12 @@
-"""The surrounding operators at the ends of their ranges: moments that are not numbers."""
+"""The surrounding operators at the ends of their ranges: moments that are not numbers, temporaries on a stream that
+is not the current one."""
 import numpy as np
 import pytest
 import torch
 
 from residual_binarized_weight_b200 import rbw
 from tests.test_adamw_gpu import F32, make, reference, upload
+from tests.test_linear_gpu import Case
 
 gpu = pytest.mark.gpu
 DEV = "cuda"
@@ -35,3 +37,68 @@ def test_a_second_moment_of_nan_stays(n, at):
     opt.step(4)
     for got in (T.exp_avg, T.exp_avg_sq, T.param):
         assert int(torch.isnan(got.float()).sum()) == 1 and bool(torch.isnan(got.float())[at])
+
+
+# ---------------------------------------------------------------- streams
+def delay(cycles=40_000_000):
+    """Some 20 ms of idling on the current stream."""
+    torch.cuda._sleep(cycles)
+
+
+def stream_case(which):
+    """(call(stream), bytes of the workspace that it makes itself)"""
+    if which == "backward":
+        M, N = 3000, 1000
+        d = torch.randn(M, N, device=DEV).bfloat16()
+        return lambda s: rbw.epilogue_backward(d, d, act="silu", stream=s)[2], rbw.epilogue_backward_workspace_bytes(M, N)
+    M, N, K = (2600, 4100, 1056) if which == "dense" else (300, 512, 1024)
+    if which in ("qat", "forward"):
+        W = torch.randn(N, K, device=DEV) * 0.02
+        g, h = rbw.svid_greedy(W, 2, 5)
+        X = torch.randn(M, K, device=DEV).bfloat16()
+        if which == "forward":
+            return lambda s: rbw.qat_forward(W, g, h, 2, X, stream=s), rbw.qat_forward_workspace_bytes(N, K, 2, M)
+        return lambda s: rbw.qat_linear(W, g, h, 2, X, stream=s), rbw.qat_linear_workspace_bytes(N, K, 2, M)
+    c = Case(M, N, K, 2)
+    return lambda s: rbw.linear(c.layer, c.X, stream=s), rbw.linear_workspace_bytes(N, K, 2, M)
+
+
+@gpu
+@pytest.mark.parametrize("which", ["linear", "dense", "qat", "forward", "backward"])
+def test_temporaries_belong_to_the_given_stream(which):
+    """The workspace that a call on another stream makes for itself is not given to the current stream while that call
+    is still to run: what the current stream then allocates and fills keeps its values."""
+    call, nbytes = stream_case(which)
+    want = call(None)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        delay()
+    got = call(s)
+    mine = [torch.full((max(nbytes // d, 16),), 77, dtype=torch.uint8, device=DEV) for d in (1, 1, 2, 4)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    for t in mine:
+        assert bool((t == 77).all())
+
+
+@gpu
+@pytest.mark.parametrize("which", ["linear", "dense", "qat", "forward", "backward"])
+def test_results_of_another_stream_outlive_their_readers(which):
+    """A result made on another stream and dropped while the current stream still has to read it is not overwritten
+    by the next call's."""
+    call, _ = stream_case(which)
+    want = call(None).clone()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    got = call(s)
+    torch.cuda.current_stream().wait_stream(s)
+    delay()
+    copy = got.clone()
+    del got
+    with torch.cuda.stream(s):
+        junk = [torch.full_like(want, 5.0) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want) and all(bool((t == 5).all()) for t in junk)
