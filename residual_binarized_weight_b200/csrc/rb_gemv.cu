@@ -898,7 +898,8 @@ constexpr int kLutBuildTiles = 8;
 
 // Single layer (count == 1): lowest latency.  Slices per CTA = ceil(S/16),
 // CS = ceil(S / that) CTAs per cluster, row chunks (R): one cluster fewer than
-// the SMs hold at one CTA each (and no more than stay resident), one wave.
+// the SMs hold at one CTA each (and no more than stay resident), one wave;
+// more, in several waves, where the rows need them to fit in shared memory.
 // Batch: CS (a power of two) and R minimise the modelled time waves * (time of
 // one CTA), where a CTA builds ceil(S/CS) tables and runs ceil(rows/R) row
 // tiles through each, and the count * R clusters run in ceil(count * R /
@@ -928,10 +929,8 @@ rb_status lut_plan_uncached(int N, int K, int count, LutPlan* plan)
         LutPlan p{CS, R, lut_table_bytes(KP) + lut_row_bytes(Nt, R, CS)};
         if (CS > 1) {
             const int active = lut_resident<KP>(CS, p.smem);
-            if (active > 0 && active < R) {
-                p.R = active;
-                p.smem = lut_table_bytes(KP) + lut_row_bytes(Nt, p.R, CS);
-            }
+            const int smem = active > 0 ? lut_table_bytes(KP) + lut_row_bytes(Nt, active, CS) : 0;
+            if (active > 0 && active < R && smem <= 227 * 1024) p = LutPlan{CS, active, smem};
         }
         if (p.smem > 227 * 1024) return RB_ERR_UNSUPPORTED;
         *plan = p;

@@ -1,5 +1,5 @@
-"""The surrounding operators at the ends of their ranges: moments that are not numbers, temporaries on a stream that
-is not the current one."""
+"""The surrounding operators at the ends of their ranges: layers wider than one wave of byte tables, moments that are
+not numbers, temporaries on a stream that is not the current one."""
 import numpy as np
 import pytest
 import torch
@@ -37,6 +37,35 @@ def test_a_second_moment_of_nan_stays(n, at):
     opt.step(4)
     for got in (T.exp_avg, T.exp_avg_sq, T.param):
         assert int(torch.isnan(got.float()).sum()) == 1 and bool(torch.isnan(got.float())[at])
+
+
+# ---------------------------------------------------------------- one token
+@gpu
+@pytest.mark.parametrize("N,K,k", [(128256, 4096, 3), (151936, 4096, 4), (400000, 4096, 2), (400000, 4096, 1),
+                                   (1000000, 288, 2)])
+def test_one_token_of_a_wide_layer(N, K, k):
+    """Rows that one wave of the byte-table kernel cannot hold.  Against the product of two such tokens, both within
+    their bounds of the definition: that of test_linear_gpu, and K 2^-23 of the magnitudes for the tables' fp32 sums."""
+    L = rbw.PackedLayer(N, K, k)
+    S, T = (K + 255) // 256, (N + 31) // 32
+    p = L.planes.view(k, S, T, 8, 32)
+    p.random_(-2 ** 31, 2 ** 31 - 1)
+    rows = rbw.planes_to_rowmajor(L)                           # drops what stands for absent rows and columns
+    L = rbw.planes_from_rowmajor(rows, N, K, k, out=L)
+    L.g16.copy_((torch.rand(k, N, device=DEV) + 0.5) * 0.6 ** torch.arange(k, device=DEV)[:, None])
+    L.h16.copy_(torch.randn(k, K, device=DEV) * 0.1)
+    x = torch.randn(1, K, device=DEV).bfloat16()
+    bias = torch.randn(N, device=DEV)
+    res = torch.randn(1, N, device=DEV)
+    y1 = rbw.linear(L, x, bias=bias, residual=res, y_dtype=torch.float32)
+    y2 = rbw.linear(L, x.repeat(2, 1), bias=bias, residual=res.repeat(2, 1), y_dtype=torch.float32)
+    g, h, xd = L.g16.double(), L.h16.double(), x.double()
+    size = sum((xd.abs() @ h[i].abs())[:, None] * g[i].abs() for i in range(k))
+    top = g.abs().amax(0) * xd.abs().sum()
+    tol = ((k > 1) * (k + 1) * 2.0 ** -11 + (K / 16 + 16 + K) * 2.0 ** -23) * size + (k > 1) * 2 * k * 2.0 ** -25 * top
+    tol = tol + 2.0 ** -22 * (y2[:1].double().abs() + bias.abs() + res.abs())
+    assert bool(((y1.double() - y2[:1].double()).abs() <= tol).all())
+    assert torch.equal(rbw.linear(L, x, y_dtype=torch.float32), rbw.gemv(L, x))
 
 
 # ---------------------------------------------------------------- streams
