@@ -646,31 +646,45 @@ class AdamWTensor:
     """One tensor of an AdamW step: a parameter, its gradient and its states (contiguous CUDA tensors).
 
     32-bit states: exp_avg and exp_avg_sq fp32.  8-bit: both torch.float8_e4m3fn (exp_avg_sq holding square
-    roots) with fp32 scales of ceil(n / 256) elements.  `new_state` makes fresh ones."""
+    roots) with fp32 scales of ceil(n / 256) elements.  `new_state` makes fresh ones.  Any of them, the rate and the
+    decay may be assigned anew between steps."""
+
+    _edits = 0                   # assignments to any AdamWTensor, so that a step sees at once that there were none
 
     def __init__(self, param, grad, exp_avg, exp_avg_sq, exp_avg_scale=None, exp_avg_sq_scale=None, lr=1e-3,
                  weight_decay=0.0):
         self.param, self.grad, self.exp_avg, self.exp_avg_sq = param, grad, exp_avg, exp_avg_sq
         self.exp_avg_scale, self.exp_avg_sq_scale = exp_avg_scale, exp_avg_sq_scale
         self.lr, self.weight_decay = lr, weight_decay
-        n = param.numel()
-        self.state_bits = 32 if exp_avg.dtype == torch.float32 else 8
+        self.check()
+
+    def __setattr__(self, name, value):
+        AdamWTensor._edits += 1
+        self.__dict__["edits"] = self.__dict__.get("edits", 0) + 1
+        self.__dict__[name] = value
+
+    @property
+    def state_bits(self):
+        return 32 if self.exp_avg is None or self.exp_avg.dtype == torch.float32 else 8
+
+    @property
+    def device(self):
+        return self.param.get_device()
+
+    def check(self):
+        n = self.param.numel()
         state = torch.float32 if self.state_bits == 32 else torch.float8_e4m3fn
-        for name, t, types, want in (("param", param, (torch.float32, torch.bfloat16), n),
-                                     ("grad", grad, (torch.float32, torch.bfloat16), n),
-                                     ("exp_avg", exp_avg, (state,), n), ("exp_avg_sq", exp_avg_sq, (state,), n)):
-            if t.dtype not in types or t.numel() != want or not t.is_contiguous():
-                raise ValueError("%s: expected %d contiguous elements of %s" % (name, want, " or ".join(map(str, types))))
-        self.device = param.get_device()
-        if any(t.get_device() != self.device for t in (grad, exp_avg, exp_avg_sq)):
-            raise ValueError("a parameter, its gradient and its states are on one device")
+        tensors = [("param", (torch.float32, torch.bfloat16), n), ("grad", (torch.float32, torch.bfloat16), n),
+                   ("exp_avg", (state,), n), ("exp_avg_sq", (state,), n)]
         if self.state_bits == 8:
             blocks = (n + ADAMW_BLOCK - 1) // ADAMW_BLOCK
-            for name, t in (("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale)):
-                if t is None or t.dtype != torch.float32 or t.numel() != blocks or not t.is_contiguous():
-                    raise ValueError("%s: expected %d contiguous elements of torch.float32" % (name, blocks))
-                if t.get_device() != self.device:
-                    raise ValueError("a parameter, its gradient and its states are on one device")
+            tensors += [("exp_avg_scale", (torch.float32,), blocks), ("exp_avg_sq_scale", (torch.float32,), blocks)]
+        for name, types, want in tensors:
+            t = getattr(self, name)
+            if t is None or t.dtype not in types or t.numel() != want or not t.is_contiguous():
+                raise ValueError("%s: expected %d contiguous elements of %s" % (name, want, " or ".join(map(str, types))))
+            if t.get_device() != self.device:
+                raise ValueError("a parameter, its gradient and its states are on one device")
 
     @staticmethod
     def new_state(param, bits=32):
@@ -695,23 +709,37 @@ class AdamWTensor:
 
 
 class AdamW:
-    """rb_adamw_step over a fixed list of AdamWTensor (one call for all of them).  The list's addresses, rates and
-    decays are taken when it is made; `refresh` takes them again."""
+    """rb_adamw_step over a fixed list of AdamWTensor (one call for all of them).  The table of addresses, rates and
+    decays that the library takes is kept from step to step and follows what is assigned to the AdamWTensors;
+    `refresh` makes it anew, which is needed where a tensor's memory is swapped beneath it (`t.data = ..`, `set_`)."""
 
     def __init__(self, tensors, beta1=0.9, beta2=0.999, eps=1e-8, seed=0):
-        self.tensors = list(tensors)
+        self.tensors = tuple(tensors)
         self.hyper = RbAdamW(beta1, beta2, eps, 0, seed & 0xFFFFFFFF, 0, None, None, None)
         self.refresh()
 
     def refresh(self):
+        self._table = (RbAdamWTensor * len(self.tensors))()
+        self._taken = [-1] * len(self.tensors)              # each tensor's count of assignments when its row was made
+        self._follow()
+
+    def _follow(self):
         if not self.tensors or any(t.device != self.tensors[0].device for t in self.tensors):
             raise ValueError("expected tensors of one device, at least one")
-        self._table = (RbAdamWTensor * len(self.tensors))(*[t.struct() for t in self.tensors])
+        edits = AdamWTensor._edits
+        for i, t in enumerate(self.tensors):
+            if t.edits != self._taken[i]:
+                t.check()
+                self._table[i] = t.struct()
+                self._taken[i] = t.edits
+        self._edits = edits
 
     def step(self, step, lr_scale=None, grad_scale=None, dev_status=None, flags=0, stream=None):
         """One step; `step` is its number (from 1), or an int32 CUDA tensor that holds it (for captured graphs).
         lr_scale and grad_scale: fp32 CUDA tensors of one element that multiply every lr and every gradient."""
         H = self.hyper
+        if self._edits != AdamWTensor._edits:
+            self._follow()
         dev, st = _current(stream)
         if self.tensors[0].device != dev:
             raise ValueError("the tensors are not on the current CUDA device")

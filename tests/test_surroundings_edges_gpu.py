@@ -1,5 +1,5 @@
 """The surrounding operators at the ends of their ranges: layers wider than one wave of byte tables, moments that are
-not numbers, temporaries on a stream that is not the current one."""
+not numbers, temporaries on a stream that is not the current one, gradients that are replaced between steps."""
 import numpy as np
 import pytest
 import torch
@@ -37,6 +37,27 @@ def test_a_second_moment_of_nan_stays(n, at):
     opt.step(4)
     for got in (T.exp_avg, T.exp_avg_sq, T.param):
         assert int(torch.isnan(got.float()).sum()) == 1 and bool(torch.isnan(got.float())[at])
+
+
+@gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_replaced_gradients_are_the_ones_used(bits):
+    """A gradient, rate or decay that is assigned between steps counts in the next one."""
+    ts = [make(3000, bits, F32, F32, i) for i in range(3)]
+    Ts, Rs = [upload(t) for t in ts], [upload(t) for t in ts]
+    opt = rbw.AdamW(Ts, seed=2)
+    opt.step(1)
+    rbw.AdamW(Rs, seed=2).step(1)
+    for T, R in zip(Ts[1:], Rs[1:]):
+        new = torch.randn(3000, device=DEV)
+        T.grad, R.grad = new, new
+        T.lr = R.lr = 0.5
+        T.weight_decay = R.weight_decay = 0.25
+    opt.step(2)
+    rbw.AdamW(Rs, seed=2).step(2)
+    for T, R in zip(Ts, Rs):
+        for a, b in ((T.param, R.param), (T.exp_avg, R.exp_avg), (T.exp_avg_sq, R.exp_avg_sq)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
 # ---------------------------------------------------------------- one token
