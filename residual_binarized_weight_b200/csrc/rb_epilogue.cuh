@@ -12,6 +12,28 @@ namespace rbw {
 // limit here) and so are the exponentials: their error, a few 2^-23, is far
 // below the bf16 rounding of what is stored, and the kernels that use them
 // are bound by memory or by the tensor cores.
+
+// The normal distribution function for GELU, from e = exp(-p^2 / 2):
+//   Phi(-|p|) = e t Q(t),   t = 1 / (1 + 0.3 |p|),
+// Q of degree 7, fitted to 1.4e-7 relative for |p| up to 13.5 (an exchange algorithm on erfc's scaled form; with
+// the roundings 4.5e-7), where e leaves fp32.  (1 + erf(p / sqrt 2)) / 2 would cancel below zero: 4 % off at -5.
+// erfcf has the accuracy, at a price (gradient of gelu(x + b) .* u, 2048 x 14336, in a graph: 77.1 us by erfcf, 60.4 by
+// erff, 53.7 by this, which shares e with the slope).
+__device__ __forceinline__ float normal_cdf(float p, float e)
+{
+    const float t = __fdividef(1.0f, fmaf(0.3f, fabsf(p), 1.0f));
+    float q = 0.035892046988010406f;
+    q = fmaf(q, t, -0.15811005234718323f);
+    q = fmaf(q, t, 0.20791947841644287f);
+    q = fmaf(q, t, -0.05512828379869461f);
+    q = fmaf(q, t, 0.1293278932571411f);
+    q = fmaf(q, t, 0.09968061000108719f);
+    q = fmaf(q, t, 0.12079139053821564f);
+    q = fmaf(q, t, 0.11962684988975525f);
+    q *= t * e;
+    return p > 0.0f ? 1.0f - q : q;
+}
+
 template <int ACT>
 __device__ __forceinline__ float activate(float p)
 {
@@ -20,7 +42,7 @@ __device__ __forceinline__ float activate(float p)
     } else if constexpr (ACT == RB_ACT_SILU) {
         return __fdividef(p, 1.0f + __expf(-p));
     } else if constexpr (ACT == RB_ACT_GELU) {
-        return 0.5f * p * (1.0f + erff(p * 0.70710678118654752f));
+        return p * normal_cdf(p, __expf(-0.5f * p * p));
     } else if constexpr (ACT == RB_ACT_GELU_TANH) {
         // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
         const float u = 0.79788456080286536f * (p + 0.044715f * p * p * p);
@@ -42,9 +64,10 @@ __device__ __forceinline__ void activate_slope(float p, float& a, float& d)
         a = p * q;
         d = q + a * (1.0f - q);
     } else if constexpr (ACT == RB_ACT_GELU) {
-        const float c = 0.5f * (1.0f + erff(p * 0.70710678118654752f));
+        const float e = __expf(-0.5f * p * p);
+        const float c = normal_cdf(p, e);
         a = p * c;
-        d = c + p * 0.39894228040143268f * __expf(-0.5f * p * p);
+        d = c + p * 0.39894228040143268f * e;
     } else if constexpr (ACT == RB_ACT_GELU_TANH) {
         const float p2 = p * p;
         const float u = 0.79788456080286536f * (p + 0.044715f * p2 * p);

@@ -1,11 +1,15 @@
-"""The surrounding operators at the ends of their ranges: layers wider than one wave of byte tables, moments that are
-not numbers, temporaries on a stream that is not the current one, gradients that are replaced between steps."""
+"""The surrounding operators at the ends of their ranges: tails of the activations, layers wider than one wave of byte
+tables, moments that are not numbers, temporaries on a stream that is not the current one, gradients that are replaced
+between steps."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
 from residual_binarized_weight_b200 import rbw
 from tests.test_adamw_gpu import F32, make, reference, upload
+from tests.test_epilogue_gpu import act64
 from tests.test_linear_gpu import Case
 
 gpu = pytest.mark.gpu
@@ -58,6 +62,44 @@ def test_replaced_gradients_are_the_ones_used(bits):
     for T, R in zip(Ts, Rs):
         for a, b in ((T.param, R.param), (T.exp_avg, R.exp_avg), (T.exp_avg_sq, R.exp_avg_sq)):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+# ---------------------------------------------------------------- activations
+# GELU is p Phi(p).  Below zero Phi's kernel form is a quotient (one unit of 2^-23), a polynomial (with its own
+# roundings 4 units), two products and exp(-p^2 / 2), by CUDA's bound for the fast exponential 2 + 0.6 p^2 units, whose
+# argument's rounding counts 0.25 p^2 more: less than (2 p^2 + 16) 2^-23, relative to the result wherever it lies.
+def gelu_bound(p):
+    return (2 * p * p + 16) * 2.0 ** -23
+
+
+@gpu
+@pytest.mark.parametrize("M", [1, 5, 70])
+def test_gelu_relative_to_itself(M):
+    """X is 0, so that P is the bias: the activation in fp32."""
+    N = 3277
+    c = Case(M, N, 64, 2)
+    c.layer.h16.zero_()
+    p = (torch.arange(N, device=DEV) - 1638) / 128.0           # -12.8 .. 12.8
+    Y = rbw.linear(c.layer, c.X, bias=p, act="gelu", y_dtype=torch.float32).double()
+    p = p.double()
+    want = 0.5 * p * torch.special.erfc(-p / math.sqrt(2))
+    assert bool(((Y - want).abs() <= gelu_bound(p) * want.abs()).all())
+
+
+@gpu
+@pytest.mark.parametrize("N", [200, 1640])
+def test_gelu_slope_far_below_zero(N):
+    """dP and dmul at p = 0 .. -12.8; the slope's two terms cancel near -0.75, so its bound goes by their sizes."""
+    P = (-torch.arange(N, device=DEV) * (12.8 / N)).bfloat16().expand(9, N).contiguous()
+    one = torch.ones_like(P)
+    dP, dU, db = rbw.epilogue_backward(one, P, act="gelu", mul=one)
+    p = P.double()
+    c, t = 0.5 * torch.special.erfc(-p / math.sqrt(2)), p * torch.exp(-p * p / 2) / math.sqrt(2 * math.pi)
+    a, d = act64(p, "gelu")
+    assert bool(((dU.double() - a).abs() <= (2.0 ** -8 + gelu_bound(p)) * a.abs()).all())
+    off = gelu_bound(p) * (c + t.abs())
+    assert bool(((dP.double() - d).abs() <= 2.0 ** -8 * d.abs() + off).all())
+    assert bool(((db.double() - d.sum(0)).abs() <= (off + 9 * 2.0 ** -24 * d.abs()).sum(0)).all())
 
 
 # ---------------------------------------------------------------- one token
