@@ -517,7 +517,7 @@ typedef struct {
  * Y and preact must not overlap each other or an input, except Y = residual as above
  * (RB_ERR_ARG).  Arrays of one row stride in bytes may share rows side by side (the halves
  * of a [M][2N] buffer); with different strides, address ranges that meet are refused.
- *   workspace  rb_linear_workspace_bytes(N, K, k, M) bytes (X in fp16; where
+ *   workspace  rb_linear_workspace_bytes(N, K, k, M) bytes (X in fp16 and a factor per row; where
  *              the weights are expanded once for some thousand tokens, 2 N K bytes more);
  *              no clearing needed; calls that share one must not overlap on the GPU.
  * One token, k <= 4: the byte tables of rb_gemv, with its exact products, fp32 sums and
@@ -528,8 +528,10 @@ typedef struct {
  * is off by at most (k + 1) 2^-11 sum_i |g_i h_i| (k = 1: exact), which on a product of some
  * thousand columns averages to about 2^-12 of it; in fp16's subnormal range (|h| below
  * 2^-14, expanded weights 2^-10) by up to k 2^-25 max_j |g_j|, expanded k 2^-21, more.  The
- * tensor core cuts its fp32 sums (off by some 2^-20 of the result for K = 4096).  X is
- * converted to fp16 as for rb_gemm.  RB_DEV_RANGE where X overflows and, unless the weights
+ * tensor core cuts its fp32 sums (off by some 2^-20 of the result for K = 4096).  X may have any
+ * size: each row is converted to fp16 at a power of two of its own, so that values down to 2^-31 of the
+ * row's largest are exact and smaller ones off by at most 2^-39 of it.  RB_DEV_RANGE where X holds an
+ * infinity, or a value past fp16 (65504; the result holds all the same) and, unless the weights
  * are expanded once, where |h| is above 65504 / k for k >= 2, whose sums then may.
  * dev_status otherwise as rb_gemm.
  *

@@ -30,9 +30,9 @@
 //               shares a scheduler with expansion warps, so it is kept short: the range
 //               is looked at once, on the largest |h|.
 //   warp 18     one thread loads X tiles (TMA, 128-byte swizzle), prepared by a pre-pass.
-// A pre-pass converts X to fp16, each 32-column group interleaved so
-// that columns (j, j + 16) are neighbours: then one shift brings the sign bits of
-// a pair to the sign bits of an fp16x2.
+// A pre-pass converts X to fp16, each row at a power of two of its own (rb_linear.cuh), which the
+// accumulators take back, and each 32-column group interleaved so that columns (j, j + 16) are
+// neighbours: then one shift brings the sign bits of a pair to the sign bits of an fp16x2.
 //
 // Three rings: X (shared memory, up to 8 k-blocks), sign words and h pairs (by slice), and A (tensor memory, 8
 // k-blocks).  Two k-blocks make a unit, whose MMAs are issued and whose stages are
@@ -85,18 +85,24 @@ struct LinArgs {
 // ---------------------------------------------------------------- pre-pass
 // beside: the launch before this one derives the planes of a training forward, which it does not read: it runs
 // beside it, and waits for it only before it ends (2048 x 4096 -> 4096: 97.4 us against 99.1 one after the other).
-__global__ void __launch_bounds__(256)
+template <int B, int T, int H>
+__global__ void __launch_bounds__(B)
 linear_prepass_kernel(const uint16_t* __restrict__ X, int64_t ldx, int M, int K, uint16_t* __restrict__ X16,
-                      int32_t* dev_status, bool beside)
+                      float* __restrict__ xs, int32_t* dev_status, bool beside)
 {
     pdl_launch_dependents();
     if (!beside) pdl_wait();
-    const int64_t vecs = (int64_t)K / 8, total = (int64_t)M * vecs;         // a multiple of 4
-    bool inf = false;
-    for (int64_t v0 = (int64_t)blockIdx.x * 1024; v0 < total; v0 += (int64_t)gridDim.x * 1024)
-        convert_x4(X, ldx, K, vecs, total, v0, X16, inf);
-    if (inf) set_dev_status(dev_status, RB_DEV_RANGE);
+    bool range = false;
+    convert_rows<B, T, H>(X, ldx, M, K, (int)blockIdx.x, (int)gridDim.x, X16, xs, range);
+    if (range) set_dev_status(dev_status, RB_DEV_RANGE);
     if (beside) pdl_wait();                    // so that whoever waits for this grid has waited for the planes too
+}
+template <int B, int T, int H>
+rb_status launch_prepass(const LinArgs& a, uint16_t* x16, float* xs, bool pdl, cudaStream_t stream)
+{
+    const int64_t blocks = ((int64_t)a.M + B / T - 1) / (B / T), most = 8 * 148 * 256 / B;
+    return launch(linear_prepass_kernel<B, T, H>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(B), 0, stream, pdl, a.X,
+                  a.ldx, a.M, a.K, x16, xs, a.dev_status, a.g32 != nullptr);
 }
 
 // ---------------------------------------------------------------- main kernel
@@ -124,6 +130,12 @@ __host__ inline int linear_smem(int kp, int bt, int stages, int wstages, int ks)
     int ring = stages * bt * 128;
     if (ring < kEW * kTile) ring = kEW * kTile;                // the transpose tiles reuse it
     return 1024 + ring + wstages * w_stage_bytes(kp) + kBarBytes + recv_bytes(bt, ks);
+}
+
+// xs of the sixteen tokens from c on: lane j % 16 holds the jth's.
+__device__ __forceinline__ float token_xs(const LinEp& ep, int64_t m0, int c, int tokens, int lane)
+{
+    return c + (lane & 15) < tokens ? ep.xs[m0 + c + (lane & 15)] : 0.0f;
 }
 
 __device__ __forceinline__ void sts128(uint32_t a, const uint4& v)
@@ -427,7 +439,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
         if (ok) {
             const int tokens = min(bt, A.M - m0);
-            pdl_wait();                           // what mul and residual hold
+            pdl_wait();                           // xs, what mul and residual hold
+            float xs = ks == 1 ? token_xs(A.ep, m0, part * 16, tokens, lane) : 0.0f;    // of a block's tokens, one block ahead
             if (ks == 1 && !ep_vectors(A.ep)) {
                 const float bias = A.ep.bias && n0 + r < A.N ? A.ep.bias[n0 + r] : 0.0f;
                 Column<16> f;                     // the next block's operands are fetched while this one is finished
@@ -443,7 +456,9 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
                     tc_wait_ld();
                     float y[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) y[j] = fmaf(scale, __uint_as_float(v[j]), bias);
+                    for (int j = 0; j < 16; ++j)
+                        y[j] = fmaf(scale, __uint_as_float(v[j]) * __shfl_sync(0xffffffffu, xs, j), bias);
+                    xs = token_xs(A.ep, m0, c + 4 * kEW, tokens, lane);
                     ep_finish_column(A.ep, at, left, f, y);
                     at = ep_down(at, block);
                     left -= 4 * kEW;
@@ -480,12 +495,14 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
                         const float4 lo = *reinterpret_cast<const float4*>(src);
                         const float4 hi = *reinterpret_cast<const float4*>(src + 4);
                         float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                        const float back = __shfl_sync(0xffffffffu, xs, u * 8 + (lane >> 2));
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] += bias[e];
+                        for (int e = 0; e < 8; ++e) y[e] = fmaf(y[e], back, bias[e]);
                         const EpAt pu = u == 0 ? at : ep_down(at, eight);
                         if (left > 8 * u) ep_finish(A.ep, pu, cnt, f[u], y);
                         if (left > 4 * kEW + 8 * u) ep_fetch(A.ep, ep_down(pu, block), cnt, f[u]);
                     }
+                    xs = token_xs(A.ep, m0, c + 4 * kEW, tokens, lane);
                     at = ep_down(at, block);
                     left -= 4 * kEW;
                     __syncwarp();
@@ -517,6 +534,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
         const int g0 = 16 * rank / ks, groups = 16 * (rank + 1) / ks - g0;
         const int tokens = min(bt, A.M - m0), items = groups * tokens, pitch = recv_pitch(bt);
         Eight f;
+        float back = 0.0f;                        // the token's xs
         auto item = [&](int x, bool finish) {
             const int g = x / tokens, tok = x - g * tokens;
             const int64_t n = (int64_t)n0 + 8 * (g0 + g);
@@ -524,6 +542,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
             if (cnt <= 0) return;
             const EpAt at = ep_at(A.ep, (int64_t)m0 + tok, n);
             if (!finish) {
+                back = A.ep.xs[m0 + tok];
                 ep_fetch(A.ep, at, cnt, f);
                 return;
             }
@@ -534,7 +553,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_consta
                 for (int e = 0; e < 8; ++e) y[e] += src[e * pitch];
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] += A.ep.bias && e < cnt ? A.ep.bias[n + e] : 0.0f;
+            for (int e = 0; e < 8; ++e) y[e] = fmaf(y[e], back, A.ep.bias && e < cnt ? A.ep.bias[n + e] : 0.0f);
             ep_finish(A.ep, at, cnt, f, y);
         };
         __syncwarp();
@@ -656,7 +675,7 @@ rb_status launch_tc(const LinArgs& args, const uint16_t* x16, int ks, cudaStream
 
 size_t run_workspace(int N, int K, int kp, int M)
 {
-    return plan(N, K, kp, M).dense ? dense_workspace(N, K, M) : ((size_t)M * K * 2 + 255) / 256 * 256;
+    return plan(N, K, kp, M).dense ? dense_workspace(N, K, M) : x16_bytes(M, K) + xs_bytes(M);
 }
 
 // a: planes, row scales, X, h, epilogue, sizes
@@ -671,10 +690,12 @@ rb_status linear_run(LinArgs a, int kp, void* workspace, bool pdl, cudaStream_t 
     a.kb_per = p.kb_per;
     a.limit = kp > 1 || a.h32 ? 65504.0f / (float)kp : HUGE_VALF;
     uint16_t* x16 = static_cast<uint16_t*>(workspace);
-    int64_t xblocks = ((int64_t)a.M * (a.K / 8) + 1023) / 1024;
-    if (xblocks > 8 * 148) xblocks = 8 * 148;
-    const rb_status st = launch(linear_prepass_kernel, dim3((unsigned)xblocks), dim3(256), 0, stream, pdl || a.g32, a.X,
-                                a.ldx, a.M, a.K, x16, a.dev_status, a.g32 != nullptr);
+    float* xs = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + x16_bytes(a.M, a.K));
+    a.ep.xs = xs;
+    const bool dependent = pdl || a.g32;
+    const rb_status st = a.K <= 1024   ? launch_prepass<256, 32, 4>(a, x16, xs, dependent, stream)
+                         : a.K <= 4096 ? launch_prepass<256, 128, 4>(a, x16, xs, dependent, stream)
+                                       : launch_prepass<512, 512, 4>(a, x16, xs, dependent, stream);
     if (st != RB_OK) return st;
     switch (kp) {
         case 1: return launch_tc<1>(a, x16, p.ks, stream);

@@ -21,6 +21,7 @@ struct LinEp {
     void* Y;
     int64_t ld_mul, ld_res, ld_pre, ld_y;
     int act, res_bf16, y_bf16;
+    const float* xs;                           // [M] what a token's accumulators are multiplied by (X in fp16, below)
     int vec;                                   // 1, 2, 4, 8: rows of mul, residual, preact, Y start on 16 bytes
 };
 
@@ -67,21 +68,25 @@ __device__ __forceinline__ bool elect_one()
 }
 
 // ---------------------------------------------------------------- X in fp16
-// X16[m][32 q + 2 j + e] = fp16(X[m][32 q + j + 16 e]).  Four lanes share a
-// 32-column group, eight columns each; a lane and its neighbour two further on
-// exchange half of theirs.
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v, bool& inf)
+// X16[m][32 q + 2 j + e] = fp16(X[m][32 q + j + 16 e] 2^s),   xs[m] = 2^-s,
+// s by row, so that its largest value comes to lie in [2^14, 2^15): a token's accumulators times xs are its products,
+// exactly, and gradients of 1e-9 or outliers of 1e6 lose nothing against values of 1.  A value keeps all its bits
+// down to 2^-31 of the row's largest, and is off by at most 2^-39 of that below.  A row with an infinity or NaN,
+// of which no product is finite, takes the smallest s.
+//
+// T of a CTA's B threads take a row, with H vectors of eight columns each in flight; of a row longer than those
+// (K > 16384) the second look comes from L2.  In a vector's group of four lanes (32 columns), a lane and its neighbour
+// two further on exchange half of theirs.
+__device__ __forceinline__ uint32_t scaled_f16x2(uint32_t v, float s)
 {
-    const __half2 h = __floats2half2_rn(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-    const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
-    inf |= (u & 0x7fffu) == 0x7c00u || (u & 0x7fff0000u) == 0x7c000000u;
-    return u;
+    const __half2 h = __floats2half2_rn(__uint_as_float(v << 16) * s, __uint_as_float(v & 0xffff0000u) * s);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ uint4 interleave(const uint4& in, int lane, bool& inf)
+__device__ __forceinline__ uint4 interleave(const uint4& in, int lane, float s)
 {
-    const uint32_t c0 = bf16x2_to_f16x2(in.x, inf), c1 = bf16x2_to_f16x2(in.y, inf);
-    const uint32_t c2 = bf16x2_to_f16x2(in.z, inf), c3 = bf16x2_to_f16x2(in.w, inf);
+    const uint32_t c0 = scaled_f16x2(in.x, s), c1 = scaled_f16x2(in.y, s);
+    const uint32_t c2 = scaled_f16x2(in.z, s), c3 = scaled_f16x2(in.w, s);
     const bool hi = lane & 2;                  // columns 16.. of the group
     const uint32_t p0 = __shfl_xor_sync(0xffffffffu, hi ? c0 : c2, 2);
     const uint32_t p1 = __shfl_xor_sync(0xffffffffu, hi ? c1 : c3, 2);
@@ -89,32 +94,77 @@ __device__ __forceinline__ uint4 interleave(const uint4& in, int lane, bool& inf
     return make_uint4(prmt(a0, b0, 0x5410), prmt(a0, b0, 0x7632), prmt(a1, b1, 0x5410), prmt(a1, b1, 0x7632));
 }
 
-// ---------------------------------------------------------------- epilogue
-// Vectors v0 + 256 u + thread, u = 0..3, of X's total (a multiple of 4), converted and interleaved.
-__device__ __forceinline__ void convert_x4(const uint16_t* __restrict__ X, int64_t ldx, int K, int64_t vecs, int64_t total,
-                                           int64_t v0, uint16_t* __restrict__ X16, bool& inf)
+constexpr uint32_t kOverF16 = 0x4780u, kInfBf16 = 0x7f80u;     // bf16 65536, the first that fp16 has not, and infinity
+__device__ __forceinline__ bool any_over(const uint4& v)
 {
-    uint4 in[4];
-    int64_t at[4];
-    const int64_t mb = v0 / vecs;              // (uniform; the lanes' own divisions are 32-bit)
-    const uint32_t qb = (uint32_t)(v0 - mb * vecs);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    bool r = false;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int64_t v = v0 + u * 256 + threadIdx.x;
-        const uint32_t x = qb + u * 256 + threadIdx.x, dm = x / (uint32_t)vecs;
-        const int64_t m = mb + dm, q = x - dm * (uint32_t)vecs;
-        at[u] = v < total ? m * K + (q & ~(int64_t)3) * 8 : -1;
-        in[u] = v < total ? __ldcs(reinterpret_cast<const uint4*>(X + m * ldx + q * 8)) : make_uint4(0, 0, 0, 0);
-    }
-    const int lane = threadIdx.x & 31, t = lane & 3;
+    for (int q = 0; q < 4; ++q)
+        r |= (w[q] & 0x7fffu) - kOverF16 <= kInfBf16 - kOverF16 || ((w[q] >> 16) & 0x7fffu) - kOverF16 <= kInfBf16 - kOverF16;
+    return r;
+}
+
+template <int B, int T, int H>
+__device__ __forceinline__ void convert_rows(const uint16_t* __restrict__ X, int64_t ldx, int M, int K, int block, int blocks,
+                                             uint16_t* __restrict__ X16, float* __restrict__ xs, bool& range)
+{
+    __shared__ uint32_t tops[B / 32];
+    constexpr int R = B / T, W = T / 32;     // rows per CTA, warps per row
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tr = threadIdx.x % T, vecs = K / 8;   // vecs: a multiple of 4
+    for (int64_t m0 = (int64_t)block * R; m0 < M; m0 += (int64_t)blocks * R) {
+        const int64_t m = m0 + threadIdx.x / T;
+        const int mine = m < M ? vecs : 0;
+        const uint16_t* src = X + m * ldx;
+        uint4 in[H];
+        auto load = [&](int b) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const uint4 o = interleave(in[u], lane, inf);
-        if (at[u] >= 0)                        // lanes 0, 2, 1, 3 of four hold cells 0-3, 4-7, 8-11, 12-15
-            *reinterpret_cast<uint4*>(X16 + at[u] + ((t >> 1) | ((t & 1) << 1)) * 8) = o;
+            for (int u = 0; u < H; ++u) {
+                const int v = b + u * T + tr;
+                in[u] = v < mine ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)v * 8)) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        uint32_t two = 0;                      // the largest |bf16|, of even and of odd columns
+        for (int b = 0; b < vecs; b += T * H) {
+            load(b);
+#pragma unroll
+            for (int u = 0; u < H; ++u) {
+                two = __vmaxu2(two, __vmaxu2(in[u].x & 0x7fff7fffu, in[u].y & 0x7fff7fffu));
+                two = __vmaxu2(two, __vmaxu2(in[u].z & 0x7fff7fffu, in[u].w & 0x7fff7fffu));
+            }
+        }
+        uint32_t top = __reduce_max_sync(0xffffffffu, max(two & 0xffffu, two >> 16));
+        if constexpr (W > 1) {
+            __syncthreads();                   // the row before has been read
+            if (lane == 0) tops[warp] = top;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < W; ++w) top = max(top, tops[warp / W * W + w]);
+        }
+        // biased exponents: 2^s brings the largest's to 127 + 14; 2^127 at most (values below 2^-113)
+        const uint32_t up = min(268u - min(top >> 7, 254u), 254u), down = 254u - up;
+        const float s = __uint_as_float(up << 23);
+        if (tr == 0 && m < M) xs[m] = __uint_as_float(down ? down << 23 : 0x00400000u);
+        const bool nan = top > kInfBf16;       // (hides what else there is)
+        range |= top >= kOverF16 && !nan;
+        for (int b = 0; b < vecs; b += T * H) {
+            if (vecs > T * H) load(b);
+#pragma unroll
+            for (int u = 0; u < H; ++u) {
+                if (nan) range |= any_over(in[u]);
+                const uint4 o = interleave(in[u], lane, s);
+                const int v = b + u * T + tr;
+                if (v < mine)                  // lanes 0, 2, 1, 3 of four hold cells 0-3, 4-7, 8-11, 12-15
+                    *reinterpret_cast<uint4*>(X16 + m * K + (int64_t)((v & ~3) | ((v >> 1) & 1) | ((v & 1) << 1)) * 8) = o;
+            }
+        }
     }
 }
 
+inline size_t x16_bytes(int M, int K) { return ((size_t)M * K * 2 + 255) / 256 * 256; }
+inline size_t xs_bytes(int M) { return ((size_t)M * 4 + 255) / 256 * 256; }
+
+// ---------------------------------------------------------------- epilogue
 template <int ACT, int CNT>
 __device__ __forceinline__ void act_all(float (&y)[CNT])
 {

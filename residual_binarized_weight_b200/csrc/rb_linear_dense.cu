@@ -5,7 +5,7 @@
 // (rb_linear.cu); from some hundred tokens on it is cheaper to write the expanded
 // matrix once, 2 bytes per weight, and let TMA bring both operands.
 //
-// Pass 1 (expand_kernel): X16 = fp16(X) and W16[n][c] = fp16(sum_i (g_i[n] 2^-e) (B_i h_i[c])),
+// Pass 1 (expand_kernel): X16 = fp16(X), rows at powers of two of their own (rb_linear.cuh), and W16[n][c] = fp16(sum_i (g_i[n] 2^-e) (B_i h_i[c])),
 // scale[n] = 2^e with k max_i |g_i| <= 2^e, so that no sum overflows and the
 // ratios of fp16 scales are exact; k = 1: W16 = +-h, scale = g, exact.  Both
 // matrices hold each 32-column group in the order 0, 16, 1, 17, ..: the signs of
@@ -167,17 +167,17 @@ __device__ __forceinline__ void expand_block(const DenseArgs& d, int64_t blk, ui
 template <int KP>
 __global__ void __launch_bounds__(256)
 expand_kernel(const __grid_constant__ DenseArgs d, int xblocks, int64_t wblocks, uint16_t* __restrict__ X16,
-              uint16_t* __restrict__ W16, float* __restrict__ scale)
+              uint16_t* __restrict__ W16, float* __restrict__ scale, float* __restrict__ xs)
 {
     pdl_launch_dependents();
     pdl_wait();
     int flags = 0;
     if ((int)blockIdx.x < xblocks) {
-        const int64_t vecs = (int64_t)d.K / 8, total = (int64_t)d.M * vecs;
-        bool inf = false;
-        for (int64_t v0 = (int64_t)blockIdx.x * 1024; v0 < total; v0 += (int64_t)xblocks * 1024)
-            convert_x4(d.X, d.ldx, d.K, vecs, total, v0, X16, inf);
-        if (inf) flags |= RB_DEV_RANGE;
+        bool range = false;
+        if (d.K <= 1024) convert_rows<256, 32, 4>(d.X, d.ldx, d.M, d.K, (int)blockIdx.x, xblocks, X16, xs, range);
+        else if (d.K <= 4096) convert_rows<256, 128, 4>(d.X, d.ldx, d.M, d.K, (int)blockIdx.x, xblocks, X16, xs, range);
+        else convert_rows<256, 256, 8>(d.X, d.ldx, d.M, d.K, (int)blockIdx.x, xblocks, X16, xs, range);
+        if (range) flags |= RB_DEV_RANGE;
     } else {
         expand_block<KP>(d, (int64_t)blockIdx.x - xblocks, W16, scale, flags);
     }
@@ -255,6 +255,8 @@ __device__ __forceinline__ void dense_epilogue(const DenseKernelArgs& A, uint8_t
                 }
             }
         }
+        const int64_t token = m - rr + lane;      // whose accumulators this lane reads
+        const float xs = token < A.M ? __ldg(A.ep.xs + token) : 0.0f;
         if (!wait_warp(acc_full + 8u * buf, (it >> 1) & 1, abort_flag, A.dev_status)) break;
         tc_fence_after();
         for (int c = hh * 32; c < cend; c += 64) {
@@ -280,7 +282,9 @@ __device__ __forceinline__ void dense_epilogue(const DenseKernelArgs& A, uint8_t
             tc_wait_ld();
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<uint4*>(tile + lane * kDPitch + 4 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                *reinterpret_cast<float4*>(tile + lane * kDPitch + 4 * e) =
+                    make_float4(__uint_as_float(v[4 * e]) * xs, __uint_as_float(v[4 * e + 1]) * xs,
+                                __uint_as_float(v[4 * e + 2]) * xs, __uint_as_float(v[4 * e + 3]) * xs);
             __syncwarp();
             EpAt p = at;
             if constexpr (VEC) {
@@ -364,7 +368,7 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_launch_dependents();
-    pdl_wait();                                   // X16, W16, scale
+    pdl_wait();                                   // X16, W16, scale, xs
 
     if (warp == kDEW + 1) {
         if (lane == 0) {                          // ---------------- TMA
@@ -447,26 +451,28 @@ struct DenseWs {
     uint16_t* x16;
     uint16_t* w16;
     float* scale;
+    float* xs;
     size_t bytes;
 };
 DenseWs dense_layout(int N, int K, int M, void* base)
 {
-    const size_t xb = ((size_t)M * K * 2 + 255) / 256 * 256, wb = ((size_t)N * K * 2 + 255) / 256 * 256;
+    const size_t xb = x16_bytes(M, K), wb = ((size_t)N * K * 2 + 255) / 256 * 256;
     const size_t sb = ((size_t)N * 4 + 255) / 256 * 256;
     char* p = static_cast<char*>(base);
     return DenseWs{reinterpret_cast<uint16_t*>(p), reinterpret_cast<uint16_t*>(p + xb),
-                   reinterpret_cast<float*>(p + xb + wb), xb + wb + sb};
+                   reinterpret_cast<float*>(p + xb + wb), reinterpret_cast<float*>(p + xb + wb + sb), xb + wb + sb + xs_bytes(M)};
 }
 
 template <int KP>
 rb_status launch_expand(const DenseArgs& d, const DenseWs& ws, bool pdl, cudaStream_t stream)
 {
-    int64_t xblocks = ((int64_t)d.M * (d.K / 8) + 1023) / 1024;
+    const int rows = d.K <= 1024 ? 8 : d.K <= 4096 ? 2 : 1;
+    int64_t xblocks = ((int64_t)d.M + rows - 1) / rows;
     if (xblocks > 4 * 148) xblocks = 4 * 148;
     const int64_t wblocks = (((int64_t)d.N + 127) / 128) * num_slices(d.K);
     if (xblocks + wblocks > INT32_MAX) return RB_ERR_UNSUPPORTED;
     return launch(expand_kernel<KP>, dim3((unsigned)(xblocks + wblocks)), dim3(256), 0, stream, pdl, d, (int)xblocks,
-                  wblocks, ws.x16, ws.w16, ws.scale);
+                  wblocks, ws.x16, ws.w16, ws.scale, ws.xs);
 }
 
 }  // namespace
@@ -509,6 +515,7 @@ rb_status dense_run(const DenseArgs& d, const void* epilogue, void* workspace, b
     if (st != RB_OK) return st;
     DenseKernelArgs a;
     a.ep = *static_cast<const LinEp*>(epilogue);
+    a.ep.xs = ws.xs;
     a.scale = ws.scale;
     a.dev_status = d.dev_status;
     a.N = d.N;

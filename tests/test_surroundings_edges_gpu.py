@@ -1,6 +1,6 @@
-"""The surrounding operators at the ends of their ranges: tails of the activations, layers wider than one wave of byte
-tables, moments that are not numbers, temporaries on a stream that is not the current one, gradients that are replaced
-between steps."""
+"""The surrounding operators at the ends of their ranges: tails of the activations, activations far below and above
+fp16, layers wider than one wave of byte tables, moments that are not numbers, temporaries on a stream that is not the
+current one, gradients that are replaced between steps."""
 import math
 
 import numpy as np
@@ -100,6 +100,108 @@ def test_gelu_slope_far_below_zero(N):
     off = gelu_bound(p) * (c + t.abs())
     assert bool(((dP.double() - d).abs() <= 2.0 ** -8 * d.abs() + off).all())
     assert bool(((db.double() - d.sum(0)).abs() <= (off + 9 * 2.0 ** -24 * d.abs()).sum(0)).all())
+
+
+# ---------------------------------------------------------------- activations out of fp16's range
+def rescaled(c, scale):
+    """The case with row m of X times scale[m]: X, the exact product and its bound.  The bound is Case's without its
+    absolute part: planes' ratios and sums (k >= 2), the tensor core's sums; all in proportion to the row."""
+    c.X = (c.X.double() * scale[:, None]).bfloat16()
+    planes = rbw.planes_to_rowmajor(c.layer).cpu().numpy().view(np.uint8)
+    b = torch.from_numpy(np.unpackbits(planes, bitorder="little").reshape(c.k, c.N, c.K)).to(DEV)
+    x, h, g = c.X.double(), c.h.double(), c.g.double()
+    c.z = sum(((x * h[i]) @ (b[i].double() * 2 - 1).T) * g[i] for i in range(c.k))
+    size = sum((x.abs() @ h[i].abs())[:, None] * g[i].abs() for i in range(c.k))
+    top = g.abs().amax(0) * x.abs().sum(1, keepdim=True)
+    c.slack = ((c.k > 1) * (c.k + 1) * 2.0 ** -11 + (c.K / 16 + 16) * 2.0 ** -23) * size + \
+        (c.k > 1) * 2 * c.k * 2.0 ** -21 * top
+    return c
+
+
+FORMS = [(1, 300, 544, 2), (2, 300, 544, 2), (9, 203, 320, 1), (64, 700, 4128, 2), (333, 264, 96, 3), (9, 128, 11008, 2),
+         (5, 64, 20032, 2), (2600, 4104, 1056, 2), (2048, 8191, 160, 2)]
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K,k", FORMS)
+def test_rows_of_any_size(M, N, K, k):
+    """Rows of X from 1e-37 to 1e5, as gradients and outliers have them."""
+    c = Case(M, N, K, k, seed=M)
+    e = torch.tensor([0.0, -4, -6, -9, -15, -25, -37, -8, -7, -5], device=DEV, dtype=torch.float64)
+    rescaled(c, 10.0 ** e.repeat((M + 9) // 10)[:M])
+    st = torch.zeros(4, dtype=torch.int32, device=DEV)
+    Y = rbw.linear(c.layer, c.X, y_dtype=torch.float32, dev_status=st)
+    off = (Y.double() - c.z).abs() - c.slack - 2.0 ** -23 * c.z.abs() - 2.0 ** -148
+    assert bool((off <= 0).all()), float(off.max())
+    assert int(st[0]) == 0
+    Z = rbw.linear(c.layer, c.X, residual=Y, y_dtype=torch.float32)       # the epilogue goes on from the scaled row
+    assert bool(((Z.double() - 2 * Y.double()).abs() <= 2.0 ** -23 * Y.double().abs()).all())
+    wide = (c.X.double() * 1e4).bfloat16()
+    ok = wide.float().abs().amax(1) > 65536
+    rescaled(c, torch.full((M,), 1e4, device=DEV, dtype=torch.float64))
+    Y = rbw.linear(c.layer, c.X, y_dtype=torch.float32, dev_status=st)
+    off = (Y.double() - c.z).abs() - c.slack - 2.0 ** -23 * c.z.abs() - 2.0 ** -148
+    assert bool((off <= 0).all()), float(off.max())
+    if M == 1:
+        assert int(st[0]) == 0
+    elif bool(ok.any()):
+        assert int(st[0]) == rbw.RB_DEV_RANGE                              # reported all the same
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K,k", FORMS[1:])
+def test_small_values_beside_a_large_one(M, N, K, k):
+    """A row whose largest value meets weights of 0: what counts is 1e-8 of it."""
+    c = Case(M, N, K, k, seed=M + 1)
+    c.layer.h16[:, 5] = 0
+    c.h = c.layer.h16
+    c.X[:, 5] = 0
+    scale = torch.full((M,), 1e-8, device=DEV, dtype=torch.float64)
+    rescaled(c, scale)
+    c.X[:, 5] = 1.0
+    Y = rbw.linear(c.layer, c.X, y_dtype=torch.float32)
+    # values keep their bits down to 2^-31 of the row's largest, and are off by at most 2^-39 of it below
+    size = sum((c.h[i].double().abs().sum() * c.g[i].double().abs())[None] for i in range(k))
+    off = (Y.double() - c.z).abs() - c.slack - 2.0 ** -23 * c.z.abs() - 2.0 ** -39 * size
+    assert bool((off <= 0).all()), float(off.max())
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K,k", FORMS[1:])
+def test_rows_that_are_not_finite(M, N, K, k):
+    """An infinity or NaN stays in its row; an infinity is reported, a NaN shows itself."""
+    c = Case(M, N, K, k, seed=M + 2)
+    c.layer.h16.abs_().clamp_min_(1e-3)
+    clean = rbw.linear(c.layer, c.X, y_dtype=torch.float32)
+    for bad, flag in ((float("inf"), rbw.RB_DEV_RANGE), (float("nan"), 0)):
+        X = c.X.clone()
+        X[1, K // 2] = bad
+        X[1, K - 1] = 1e30
+        st = torch.zeros(4, dtype=torch.int32, device=DEV)
+        Y = rbw.linear(c.layer, X, y_dtype=torch.float32, dev_status=st)
+        assert not bool(torch.isfinite(Y[1]).any())
+        assert int(st[0]) == rbw.RB_DEV_RANGE                              # (1e30 is above fp16, too)
+        keep = torch.arange(M, device=DEV) != 1
+        assert torch.equal(Y[keep], clean[keep])
+        if bad == bad:
+            assert bool((Y[1] == float("inf")).logical_or(Y[1] == -float("inf")).all())
+        X[1, K - 1] = 0
+        st.zero_()
+        rbw.linear(c.layer, X, dev_status=st)
+        assert int(st[0]) == flag
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(70, 290, 480), (2600, 4100, 1056)])
+def test_small_rows_of_a_training_forward(M, N, K):
+    W = torch.randn(N, K, device=DEV) * 0.02
+    g, h = rbw.svid_greedy(W, 2, 10)
+    X = torch.randn(M, K, device=DEV).bfloat16()
+    s = 2.0 ** -60
+    pre = [torch.empty(M, N, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    a = rbw.qat_linear(W, g, h, 2, X, preact=pre[0], y_dtype=torch.float32)
+    b = rbw.qat_linear(W, g, h, 2, X * s, preact=pre[1], y_dtype=torch.float32)
+    assert torch.equal(a * s, b) and torch.equal(pre[0] * s, pre[1])       # scaled by a power of two: bit for bit
 
 
 # ---------------------------------------------------------------- one token
