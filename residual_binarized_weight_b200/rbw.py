@@ -514,7 +514,10 @@ def _matrix(t, name, M, N, dev, dtypes=_BF16):
     return t.data_ptr(), ld
 
 
-def _vector(t, name, n, dev, dtype=torch.float32):
+def _vector(t, name, n, dev, dtype=torch.float32, shape=None):
+    """Address of a contiguous tensor of n elements, or of the given shape."""
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError("%s: expected a tensor of shape %s" % (name, shape))
     if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError("%s: expected a contiguous %s tensor of %d elements" % (name, dtype, n))
     if t.get_device() != dev:
@@ -595,8 +598,8 @@ def qat_linear(W, g, h, k_planes, X, Y=None, bias=None, act="none", mul=None, re
         ws = _scratch(qat_linear_workspace_bytes(N, K, k_planes, M), X.device, stream)
     if ws.get_device() != dev:
         raise ValueError("ws: expected a tensor on the current CUDA device")
-    st = lib().rb_qat_linear(_vector(W, "W", N * K, dev), _vector(g, "g", k_planes * N, dev),
-                             _vector(h, "h", k_planes * K, dev), N, K, k_planes, xp, ldx, M, ctypes.byref(E), yp, ldy,
+    st = lib().rb_qat_linear(_vector(W, "W", N * K, dev), _vector(g, "g", k_planes * N, dev, shape=(k_planes, N)),
+                             _vector(h, "h", k_planes * K, dev, shape=(k_planes, K)), N, K, k_planes, xp, ldx, M, ctypes.byref(E), yp, ldy,
                              RB_BF16 if Y.dtype is torch.bfloat16 else RB_F32, ws.data_ptr(), ws.nbytes,
                              _status(dev_status, dev), flags, st)
     _check("rb_qat_linear", st)
@@ -683,6 +686,8 @@ class AdamWTensor:
             t = getattr(self, name)
             if t is None or t.dtype not in types or t.numel() != want or not t.is_contiguous():
                 raise ValueError("%s: expected %d contiguous elements of %s" % (name, want, " or ".join(map(str, types))))
+            if want == n and t.dim() > 1 and self.param.dim() > 1 and t.shape != self.param.shape:
+                raise ValueError("%s: expected the parameter's shape, or one dimension" % name)
             if t.get_device() != self.device:
                 raise ValueError("a parameter, its gradient and its states are on one device")
 

@@ -55,3 +55,26 @@ def test_a_list_stays_as_it_was_made():
     assert len(opt.tensors) == 2
     with pytest.raises(TypeError):
         opt.tensors[0] = tensor()
+
+
+def test_shapes_count_and_not_only_element_numbers(monkeypatch):
+    """Scales and gradients whose elements would pair up wrongly; flat states and flat gradients still fit."""
+    monkeypatch.setattr(rbw, "_current", lambda stream: (-1, 0))
+    N, K, k = 64, 96, 2
+    W, X = torch.zeros(N, K), torch.zeros(3, K, dtype=torch.bfloat16)
+    g, h = torch.zeros(k, N), torch.zeros(k, K)
+    for bad in (dict(g=torch.zeros(N, k)), dict(g=torch.zeros(k * N)), dict(h=torch.zeros(K, k)), dict(h=torch.zeros(1, k * K))):
+        a = dict(g=g, h=h) | bad
+        with pytest.raises(ValueError):
+            rbw.qat_linear(W, a["g"], a["h"], k, X)
+    p = torch.zeros(6, 50)
+    state = rbw.AdamWTensor.new_state(p)
+    for shape in ((50, 6), (300, 1), (3, 100)):
+        with pytest.raises(ValueError):
+            rbw.AdamWTensor(p, torch.zeros(shape), **state)
+        with pytest.raises(ValueError):
+            rbw.AdamWTensor(p, torch.zeros(6, 50), **(state | dict(exp_avg=torch.zeros(shape))))
+    rbw.AdamWTensor(p, torch.zeros(6, 50), **state)
+    rbw.AdamWTensor(p, torch.zeros(300), **state)
+    rbw.AdamWTensor(torch.zeros(300), torch.zeros(6, 50), **state)
+    rbw.AdamWTensor(p, torch.zeros(6, 50), **rbw.AdamWTensor.new_state(p, 8))
