@@ -514,8 +514,8 @@ typedef struct {
  *   X    [M][K] bf16, row stride ldx elements (a multiple of 8, at least K).
  *   ep   nullable: Y = P = X What^T.
  *   Y    [M][N] fp32 or bf16, row stride ldy.
- * Y and preact must not overlap each other or an input, except Y = residual as above
- * (RB_ERR_ARG).  Arrays of one row stride in bytes may share rows side by side (the halves
+ * Y and preact must not overlap each other, an input (the layer's arrays among them) or the
+ * workspace, except Y = residual as above (RB_ERR_ARG).  Arrays of one row stride in bytes may share rows side by side (the halves
  * of a [M][2N] buffer); with different strides, address ranges that meet are refused.
  *   workspace  rb_linear_workspace_bytes(N, K, k, M) bytes (X in fp16 and a factor per row; where
  *              the weights are expanded once for some thousand tokens, 2 N K bytes more);
@@ -561,8 +561,8 @@ RB_API rb_status rb_qat_linear(const float *W, const float *g, const float *h, i
  *   mul          [M][N] bf16, row stride ld_mul; NULL: 1 (dmul must then be NULL).
  *   dP, dmul     out, [M][N] bf16, row strides ld_dp, ld_dmul; dmul nullable.
  *                dP may be dY or preact itself and dmul may be mul itself (same
- *                address and stride); no other overlap of an output (as for rb_linear,
- *                halves of one buffer may lie side by side).
+ *                address and stride); no other overlap of an output, with the workspace
+ *                neither (as for rb_linear, halves of one buffer may lie side by side).
  *   dbias        out, [N] fp32, nullable.  The sums run over the rows in a fixed
  *                order for a given shape (deterministic).
  *   workspace    rb_epilogue_backward_workspace_bytes(M, N) bytes (partial sums),

@@ -359,8 +359,11 @@ extern "C" rb_status rb_epilogue_backward(const rb_epilogue_grad_t* grad, int M,
         const MatRange rb = mat_range(g.dbias, 1, N, N, 4);
         for (const Arr& q : in)
             if (q.p && overlaps(rb, mat_range(q.p, M, N, q.ld, 2))) return RB_ERR_ARG;
+        const size_t need = rb_epilogue_backward_workspace_bytes(M, n_out);
+        if (meets(rb, workspace, need)) return RB_ERR_ARG;
         for (const Arr& q : out)
-            if (q.p && overlaps(rb, mat_range(q.p, M, N, q.ld, 2))) return RB_ERR_ARG;
+            if (q.p && (overlaps(rb, mat_range(q.p, M, N, q.ld, 2)) || meets(mat_range(q.p, M, N, q.ld, 2), workspace, need)))
+                return RB_ERR_ARG;
     }
     if (!device_is_sm100()) return RB_ERR_UNSUPPORTED;
     EbArgs a;

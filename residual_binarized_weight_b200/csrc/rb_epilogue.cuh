@@ -102,4 +102,10 @@ inline bool overlaps(const MatRange& a, const MatRange& b)
     return d < a.width || d + b.width > a.pitch;
 }
 
+// Whether an array meets n bytes at p (nothing at null).
+inline bool meets(const MatRange& a, const void* p, size_t n)
+{
+    return p && n && overlaps(a, mat_range(p, 1, (int64_t)n, (int64_t)n, 1));
+}
+
 }  // namespace rbw

@@ -44,6 +44,7 @@
 // the rank that owns them, which adds them in rank order (deterministic).
 #include <atomic>
 #include <cmath>
+#include <initializer_list>
 
 #include "rbw_internal.cuh"
 #include "rb_epilogue.cuh"
@@ -756,6 +757,19 @@ rb_status check_epilogue(const rb_epilogue_t* ep, const uint16_t* X, int64_t ldx
     return RB_OK;
 }
 
+// Whether Y or the pre-activation meets one of the call's other arrays.
+struct Bytes {
+    const void* p;
+    size_t n;
+};
+bool outputs_meet(const LinEp& ep, int64_t M, int64_t N, std::initializer_list<Bytes> others)
+{
+    const MatRange y = mat_range(ep.Y, M, N, ep.ld_y, ep.y_bf16 ? 2 : 4);
+    for (const Bytes& b : others)
+        if (meets(y, b.p, b.n) || (ep.pre && meets(mat_range(ep.pre, M, N, ep.ld_pre, 2), b.p, b.n))) return true;
+    return false;
+}
+
 // One token goes through the byte tables (4096 x 4096, k = 2: 5.9 us against 10.5 us on the tensor cores, and exact).
 bool one_token(int k_planes, int M) { return M == 1 && k_planes <= 4; }
 
@@ -795,6 +809,11 @@ extern "C" rb_status rb_linear(const rb_layer_t* layer, const uint16_t* X, int64
         if (!workspace || workspace_bytes < need) return RB_ERR_WORKSPACE;
         if (!aligned16(workspace)) return RB_ERR_ALIGN;
     }
+    const size_t kp = (size_t)layer->k_planes;
+    if (outputs_meet(a.ep, M, layer->n_out,
+                     {{layer->planes, rb_packed_words(layer->n_out, layer->k_in, layer->k_planes) * 4},
+                      {layer->g16, kp * layer->n_out * 2}, {layer->h16, kp * layer->k_in * 2}, {workspace, need}}))
+        return RB_ERR_ARG;
     if (!device_is_sm100()) return RB_ERR_UNSUPPORTED;
     if (one_token(layer->k_planes, M)) return lut_linear(layer, X, &a.ep, (flags & RB_LAUNCH_PDL) != 0, stream);
     a.planes = layer->planes;
@@ -829,6 +848,11 @@ extern "C" rb_status rb_qat_linear(const float* W, const float* g, const float* 
     if (dev_status && !aligned16(dev_status)) return RB_ERR_ALIGN;
     if (!workspace || workspace_bytes < rb_qat_linear_workspace_bytes(n_out, k_in, k_planes, M)) return RB_ERR_WORKSPACE;
     if (!aligned16(workspace)) return RB_ERR_ALIGN;
+    const size_t kp = (size_t)k_planes;
+    if (outputs_meet(a.ep, M, n_out,
+                     {{W, (size_t)n_out * k_in * 4}, {g, kp * n_out * 4}, {h, kp * k_in * 4},
+                      {workspace, rb_qat_linear_workspace_bytes(n_out, k_in, k_planes, M)}}))
+        return RB_ERR_ARG;
     if (!device_is_sm100()) return RB_ERR_UNSUPPORTED;
     uint32_t* planes = static_cast<uint32_t*>(workspace);
     const bool beside = !plan(n_out, k_in, k_planes, M).dense;    // (the dense form's first pass reads the planes)

@@ -1,10 +1,13 @@
 """What the binding of the surrounding operators checks and keeps, on host tensors (no GPU needed): nothing here
 reaches a launch."""
+import ctypes
+
 import pytest
 import torch
 
 from residual_binarized_weight_b200 import build as rbw_build
 from residual_binarized_weight_b200 import rbw
+from tests.test_surroundings_abi import A, B, K, M, N, backward, epilogue, grad, layer, linear, no_device, qat
 
 
 @pytest.fixture(autouse=True)
@@ -78,3 +81,59 @@ def test_shapes_count_and_not_only_element_numbers(monkeypatch):
     rbw.AdamWTensor(p, torch.zeros(300), **state)
     rbw.AdamWTensor(torch.zeros(300), torch.zeros(6, 50), **state)
     rbw.AdamWTensor(p, torch.zeros(6, 50), **rbw.AdamWTensor.new_state(p, 8))
+
+
+# ---------------------------------------------------------------- the C entry points, on made-up addresses
+FAR = 0x8000000                                                # planes, g16 and h16 of their own
+
+
+@pytest.fixture
+def L():
+    return rbw.lib()
+
+
+def at(**kw):
+    return ctypes.byref(epilogue(**kw))
+
+
+@pytest.mark.parametrize("name,size", [("planes", 2 * 256 * 2 * 4), ("g16", 2 * N * 2), ("h16", 2 * K * 2)])
+@pytest.mark.parametrize("m", [1, M])
+def test_outputs_over_the_layer_are_refused(L, name, size, m):
+    lay = ctypes.byref(layer(**{name: FAR}))
+    out = m * N * 2
+    for Y in (FAR, FAR + size - 16, FAR - out + 16):
+        assert linear(L, lay=lay, Y=Y, m=m) == rbw.RB_ERR_ARG
+        assert linear(L, lay=lay, ep=at(preact=Y, ld_preact=N), m=m) == rbw.RB_ERR_ARG
+
+
+@pytest.mark.parametrize("name,size", [("w", N * K * 4), ("g", 2 * N * 4), ("h", 2 * K * 4)])
+def test_outputs_over_the_latent_weight_are_refused(L, name, size):
+    for Y in (FAR, FAR + size - 16, FAR - M * N * 2 + 16):
+        assert qat(L, Y=Y, **{name: FAR}) == rbw.RB_ERR_ARG
+        assert qat(L, ep=at(preact=Y, ld_preact=N), **{name: FAR}) == rbw.RB_ERR_ARG
+
+
+def test_outputs_over_the_workspace_are_refused(L):
+    need = rbw.linear_workspace_bytes(N, K, 2, M)
+    for Y in (FAR, FAR + need - 16, FAR - M * N * 2 + 16):
+        assert linear(L, ws=FAR, Y=Y) == rbw.RB_ERR_ARG
+        assert linear(L, ws=FAR, ep=at(preact=Y, ld_preact=N)) == rbw.RB_ERR_ARG
+    need = rbw.qat_linear_workspace_bytes(N, K, 2, M)
+    for Y in (FAR, FAR + need - 16):
+        assert qat(L, ws=FAR, Y=Y) == rbw.RB_ERR_ARG
+    need = rbw.epilogue_backward_workspace_bytes(M, N)
+    for p in (FAR, FAR + (need - 1) // 16 * 16):
+        assert backward(L, grad(dP=p), ws=FAR) == rbw.RB_ERR_ARG
+        assert backward(L, grad(dmul=p), ws=FAR) == rbw.RB_ERR_ARG
+        assert backward(L, grad(dbias=p), ws=FAR) == rbw.RB_ERR_ARG
+
+
+@no_device
+def test_outputs_beside_the_layer_and_the_workspace_are_taken(L):
+    assert linear(L, ws=FAR, Y=FAR - M * N * 2) == rbw.RB_ERR_UNSUPPORTED
+    assert linear(L, ws=FAR, Y=FAR + rbw.linear_workspace_bytes(N, K, 2, M)) == rbw.RB_ERR_UNSUPPORTED
+    assert linear(L, lay=ctypes.byref(layer(planes=FAR)), Y=FAR + 4096) == rbw.RB_ERR_UNSUPPORTED
+    assert linear(L, ws=FAR, wsb=0, m=1, Y=FAR) == rbw.RB_ERR_UNSUPPORTED      # one token leaves it alone
+    assert qat(L, w=FAR, Y=FAR + N * K * 4) == rbw.RB_ERR_UNSUPPORTED
+    assert backward(L, grad(dP=A, dbias=None), ws=A) == rbw.RB_ERR_UNSUPPORTED  # no sums, no workspace
+    assert backward(L, grad(dP=B), ws=FAR) == rbw.RB_ERR_UNSUPPORTED
