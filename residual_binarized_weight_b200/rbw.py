@@ -182,6 +182,8 @@ class PackedLayer:
         self.h16 = _empty((k_planes, k_in), torch.float16, device, stream) if h16 is None else h16
         if tuple(self.g16.shape) != (k_planes, n_out) or tuple(self.h16.shape) != (k_planes, k_in):
             raise ValueError("scale tensors do not match the layer shape")
+        if any(t.dtype not in (torch.float16, torch.int16, torch.uint16) or not t.is_contiguous() for t in (self.g16, self.h16)):
+            raise ValueError("scale tensors: expected contiguous torch.float16, or its bits in 16-bit integers")
 
     def struct(self):
         return RbLayer(self.n_out, self.k_in, self.k_planes, 0, self.planes.data_ptr(),
@@ -534,6 +536,13 @@ def _status(t, dev):
     return t.data_ptr()
 
 
+def _workspace(t, dev):
+    """(address, bytes) of a workspace."""
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("ws: expected a contiguous tensor on the current CUDA device")
+    return t.data_ptr(), t.nbytes
+
+
 def _current(stream):
     """(current device, address of the given stream or of torch's current one), without making Stream objects."""
     dev = torch.cuda.current_device()
@@ -569,10 +578,11 @@ def linear(layer: PackedLayer, X, Y=None, bias=None, act="none", mul=None, resid
     E = _epilogue(M, N, dev, bias, act, mul, residual, preact)
     if ws is None:
         ws = _scratch(linear_workspace_bytes(N, K, layer.k_planes, M), X.device, stream)
-    if not layer.planes.get_device() == layer.g16.get_device() == layer.h16.get_device() == ws.get_device() == dev:
-        raise ValueError("layer and ws: expected tensors on the current CUDA device")
+    if not layer.planes.get_device() == layer.g16.get_device() == layer.h16.get_device() == dev:
+        raise ValueError("layer: expected tensors on the current CUDA device")
+    wsp, wsb = _workspace(ws, dev)
     st = lib().rb_linear(ctypes.byref(layer.struct()), xp, ldx, M, ctypes.byref(E), yp, ldy,
-                         RB_BF16 if Y.dtype is torch.bfloat16 else RB_F32, ws.data_ptr(), ws.nbytes,
+                         RB_BF16 if Y.dtype is torch.bfloat16 else RB_F32, wsp, wsb,
                          _status(dev_status, dev), flags, st)
     if st != RB_OK:
         raise RbError("rb_linear", st)
@@ -596,11 +606,10 @@ def qat_linear(W, g, h, k_planes, X, Y=None, bias=None, act="none", mul=None, re
     E = _epilogue(M, N, dev, bias, act, mul, residual, preact)
     if ws is None:
         ws = _scratch(qat_linear_workspace_bytes(N, K, k_planes, M), X.device, stream)
-    if ws.get_device() != dev:
-        raise ValueError("ws: expected a tensor on the current CUDA device")
+    wsp, wsb = _workspace(ws, dev)
     st = lib().rb_qat_linear(_vector(W, "W", N * K, dev), _vector(g, "g", k_planes * N, dev, shape=(k_planes, N)),
                              _vector(h, "h", k_planes * K, dev, shape=(k_planes, K)), N, K, k_planes, xp, ldx, M, ctypes.byref(E), yp, ldy,
-                             RB_BF16 if Y.dtype is torch.bfloat16 else RB_F32, ws.data_ptr(), ws.nbytes,
+                             RB_BF16 if Y.dtype is torch.bfloat16 else RB_F32, wsp, wsb,
                              _status(dev_status, dev), flags, st)
     _check("rb_qat_linear", st)
     return Y
@@ -626,9 +635,7 @@ def epilogue_backward(dY, preact, act="none", mul=None, bias=True, dP=None, dmul
     if dbias is not None:
         if ws is None:
             ws = _scratch(epilogue_backward_workspace_bytes(M, N), dY.device, stream)
-        if ws.get_device() != dev:
-            raise ValueError("ws: expected a tensor on the current CUDA device")
-        wsp, wsb = ws.data_ptr(), ws.nbytes
+        wsp, wsb = _workspace(ws, dev)
     yp, ldy = _matrix(dY, "dY", M, N, dev)
     pp, ldp = _matrix(preact, "preact", M, N, dev)
     up, ldu = _matrix(mul, "mul", M, N, dev)

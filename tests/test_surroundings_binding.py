@@ -83,6 +83,27 @@ def test_shapes_count_and_not_only_element_numbers(monkeypatch):
     rbw.AdamWTensor(p, torch.zeros(6, 50), **rbw.AdamWTensor.new_state(p, 8))
 
 
+def test_memory_that_is_not_in_one_piece_is_refused(monkeypatch):
+    """A workspace with gaps, whose bytes in between belong to others, and scales of another type or with gaps."""
+    monkeypatch.setattr(rbw, "_current", lambda stream: (-1, 0))
+    layer = rbw.PackedLayer(64, 96, 2, "cpu")
+    X, d = torch.zeros(3, 96, dtype=torch.bfloat16), torch.zeros(3, 64, dtype=torch.bfloat16)
+    for ws in (torch.zeros(1 << 20, 2, dtype=torch.uint8)[:, 0], torch.zeros(1 << 12, 1 << 8).t()):
+        with pytest.raises(ValueError):
+            rbw.linear(layer, X, ws=ws)
+        with pytest.raises(ValueError):
+            rbw.qat_linear(torch.zeros(64, 96), torch.zeros(2, 64), torch.zeros(2, 96), 2, X, ws=ws)
+        with pytest.raises(ValueError):
+            rbw.epilogue_backward(d, d, act="relu", ws=ws)
+    rbw.PackedLayer(64, 96, 2, "cpu", g16=torch.zeros(2, 64, dtype=torch.int16))           # bits of fp16
+    for bad in (torch.zeros(2, 64), torch.zeros(64, 2).half().t(), torch.zeros(2, 64, dtype=torch.bfloat16),
+                torch.zeros(2, 64, dtype=torch.uint8)):
+        with pytest.raises(ValueError):
+            rbw.PackedLayer(64, 96, 2, "cpu", g16=bad)
+        with pytest.raises(ValueError):
+            rbw.PackedLayer(96, 64, 2, "cpu", h16=bad)
+
+
 # ---------------------------------------------------------------- the C entry points, on made-up addresses
 FAR = 0x8000000                                                # planes, g16 and h16 of their own
 
