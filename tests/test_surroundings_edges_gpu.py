@@ -1,12 +1,13 @@
 """The surrounding operators at the ends of their ranges: tails of the activations, activations far below and above
 fp16, layers wider than one wave of byte tables, moments that are not numbers, temporaries on a stream that is not the
-current one, gradients that are replaced between steps."""
+current one, gradients that are replaced between steps, every entry point in the form that expands the weights."""
 import math
 
 import numpy as np
 import pytest
 import torch
 
+from residual_binarized_weight_b200 import build as rbw_build
 from residual_binarized_weight_b200 import rbw
 from tests.test_adamw_gpu import F32, make, reference, upload
 from tests.test_epilogue_gpu import act64
@@ -296,3 +297,179 @@ def test_results_of_another_stream_outlive_their_readers(which):
         junk = [torch.full_like(want, 5.0) for _ in range(3)]
     torch.cuda.synchronize()
     assert torch.equal(copy, want) and all(bool((t == 5).all()) for t in junk)
+
+
+# ---------------------------------------------------------------- weights expanded once
+def expanded(N, K, k, M):
+    """Whether the product runs on weights expanded in its workspace, by that workspace's size."""
+    return rbw.linear_workspace_bytes(N, K, k, M) >= 2 * N * K + 2 * M * K
+
+
+DENSE = [(2600, 4100, 1056), (2048, 8192, 160)]
+
+
+@pytest.mark.parametrize("k", [1, 2, 4])
+@pytest.mark.parametrize("M,N,K", DENSE)
+def test_these_sizes_expand_the_weights(M, N, K, k):
+    rbw_build.build()
+    assert expanded(N, K, k, M) and not expanded(N, K, k, 64)
+
+
+@gpu
+@pytest.mark.parametrize("k", [1, 2, 4])
+@pytest.mark.parametrize("M,N,K", DENSE)
+def test_latent_weight_expanded(M, N, K, k):
+    """As test_linear_gpu's test_latent_weight, with the expanded weights' subnormal step (2^-21 of the row's largest)."""
+    assert expanded(N, K, k, M)
+    W = torch.randn(N, K, generator=torch.Generator().manual_seed(k)).cuda() * 0.02
+    g, h = rbw.svid_greedy(W, k, 10)
+    c = Case(M, N, K, k, seed=4)
+    r, What, size = W.clone(), 0, 0
+    for i in range(k):
+        t = g[i][:, None] * h[i]
+        s = torch.where(r >= 0, 1.0, -1.0)
+        What = What + s.double() * g[i].double()[:, None] * h[i].double()
+        size = size + t.double().abs()
+        r = r - s * t
+    x = c.X.double()
+    c.z = x @ What.T
+    c.slack = ((k + 2) * 2.0 ** -11 + (K / 16 + 16) * 2.0 ** -23) * (x.abs() @ size.T) + \
+        (k > 1) * k * 2.0 ** -21 * g.double().abs().amax(0) * x.abs().sum(1, keepdim=True)
+    pre = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    ws = rbw.workspace(rbw.qat_linear_workspace_bytes(N, K, k, M))
+    Y = rbw.qat_linear(W, g, h, k, c.X, bias=c.bias, act="gelu_tanh", mul=c.mul, residual=c.res16, preact=pre, ws=ws)
+    c.check(Y, c.bias, "gelu_tanh", c.mul, c.res16, pre)
+    c.check(rbw.qat_linear(W, g, h, k, c.X, ws=ws, y_dtype=torch.float32), norm=False)
+    planes = rbw.pack(W, g, h, k).planes
+    assert torch.equal(ws[:4 * planes.numel()].view(torch.int32), planes)
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", DENSE)
+def test_planes_of_an_expanded_training_forward_feed_the_next_launch(M, N, K):
+    k = 2
+    assert expanded(N, K, k, M)
+    gen = torch.Generator().manual_seed(M)
+    Ws = [(torch.randn(N, K, generator=gen) * 0.02).cuda() for _ in range(3)]
+    g, h = torch.full((k, N), 0.02, device=DEV), torch.full((k, K), 0.5, device=DEV)
+    g[1] *= 0.5
+    X = torch.randn(M, K, generator=gen).bfloat16().cuda()
+    W = Ws[0].clone()
+    ws = rbw.workspace(rbw.qat_linear_workspace_bytes(N, K, k, M))
+    words = rbw.pack(W, g, h, k).planes.numel()
+    L = rbw.PackedLayer(N, K, k, planes=ws[:4 * words].view(torch.int32), g16=g.half(), h16=h.half())
+    few = X[:7]
+    ws2 = [rbw.workspace(rbw.linear_workspace_bytes(N, K, k, m)) for m in (M, 7)]
+    Y, Z = (torch.empty(M, N, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    z = torch.empty(7, N, dtype=torch.bfloat16, device=DEV)
+
+    def chain():
+        rbw.qat_linear(W, g, h, k, X, Y, ws=ws, flags=rbw.RB_LAUNCH_PDL)
+        rbw.linear(L, few, z, ws=ws2[1], flags=rbw.RB_LAUNCH_PDL)          # reads the planes before it waits
+        rbw.linear(L, X, Z, ws=ws2[0], flags=rbw.RB_LAUNCH_PDL)
+
+    chain()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for i in range(9):
+        W.copy_(Ws[i % 3])
+        graph.replay() if i % 2 else chain()
+        torch.cuda.synchronize()
+        P = rbw.pack(Ws[i % 3], g, h, k)
+        assert torch.equal(Z, rbw.linear(P, X)) and torch.equal(z, rbw.linear(P, few)), i
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", DENSE)
+def test_expanded_weights_in_a_graph_and_on_streams(M, N, K):
+    a, b = Case(M, N, K, 2, seed=1), Case(M, K, N // 32 * 32, 2, seed=2)
+    assert expanded(N, K, 2, M)
+    X = a.X.clone()
+    mid, out = torch.empty(M, N // 32 * 32 + 32, dtype=torch.bfloat16, device=DEV), torch.empty(M, K, device=DEV)
+    ws = [rbw.workspace(rbw.linear_workspace_bytes(N, K, 2, M)), rbw.workspace(rbw.linear_workspace_bytes(K, N // 32 * 32, 2, M))]
+
+    def chain():
+        rbw.linear(a.layer, X, mid[:, :N], act="silu", ws=ws[0], flags=rbw.RB_LAUNCH_PDL)
+        rbw.linear(b.layer, mid[:, :N // 32 * 32], out, ws=ws[1], flags=rbw.RB_LAUNCH_PDL)
+
+    chain()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(3):
+            chain()
+    for k in range(2):
+        X.copy_(torch.randn(M, K, generator=torch.Generator().manual_seed(k)).bfloat16())
+        g.replay()
+        torch.cuda.synchronize()
+        m = rbw.linear(a.layer, X, act="silu")
+        assert torch.equal(m, mid[:, :N])
+        assert torch.equal(rbw.linear(b.layer, m[:, :N // 32 * 32].contiguous(), y_dtype=torch.float32), out)
+    want = [rbw.linear(c.layer, c.X) for c in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append(rbw.linear((a, b)[i % 2].layer, (a, b)[i % 2].X))
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, want[i % 2]) for i, y in enumerate(got))
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", DENSE)
+def test_expanded_weights_report_what_they_meet(M, N, K):
+    k = 2
+    c = Case(M, N, K, k, seed=3)
+    st = torch.zeros(4, dtype=torch.int32, device=DEV)
+    X = c.X.clone()
+    X[M - 1, K - 1] = 1e6
+    rbw.linear(c.layer, X, dev_status=st)
+    assert int(st[0]) == rbw.RB_DEV_RANGE
+    c.layer.g16[0, 5], c.layer.g16[1, 5] = 0, float("nan")
+    bad = torch.isnan(rbw.linear(c.layer, c.X))
+    assert bool(bad[:, 5].all()) and int(bad.sum()) == M
+    W = torch.randn(N, K, device=DEV)
+    for at in (0, 21, K - 1):
+        for value, flag in ((1.0, 0), (7e4, rbw.RB_DEV_RANGE), (-float("inf"), rbw.RB_DEV_RANGE),
+                            (float("nan"), rbw.RB_DEV_NONFINITE)):
+            g, h = torch.ones(k, N, device=DEV), torch.ones(k, K, device=DEV)
+            h[k - 1, at] = value
+            st.zero_()
+            rbw.qat_linear(W, g, h, k, c.X, dev_status=st)
+            assert int(st[0]) & flag == flag and (flag or int(st[0]) == 0), (at, value, int(st[0]))
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(6000, 262176, 16416), (262200, 8192, 16416)])
+def test_expanded_weights_with_large_offsets(M, N, K):
+    """W16 past 2^32 elements, and X16."""
+    k = 2
+    assert expanded(N, K, k, M)
+    L = rbw.PackedLayer(N, K, k)
+    L.planes.zero_()                                         # -1 everywhere; the last rows' words are set below
+    words = torch.zeros(k, 64, K // 32, dtype=torch.int32, device=DEV)
+    words.random_(-2 ** 31, 2 ** 31 - 1)
+    T, S = (N + 31) // 32, (K + 255) // 256
+    small = rbw.planes_from_rowmajor(words, 64, K, k)
+    L.planes.view(k, S, T, 256)[:, :, T - 2:] = small.planes.view(k, S, 2, 256)
+    L.g16.copy_(torch.rand(k, N, device=DEV) + 0.5), L.h16.copy_(torch.randn(k, K, device=DEV) * 0.1)
+    X = torch.randn(500, K, device=DEV).bfloat16().repeat((M + 499) // 500, 1)[:M]
+    Y = rbw.linear(L, X)
+    first = Y[:500].clone()
+    assert bool((Y[:M // 500 * 500].view(-1, 500, N) == first).all())
+    assert torch.equal(Y[M // 500 * 500:], first[:M % 500])
+    del Y
+    x = X[:500].double()
+    bits = np.unpackbits(words.cpu().numpy().view(np.uint8), bitorder="little").reshape(k, 64, K)
+    sign = torch.from_numpy(bits).to(DEV).double() * 2 - 1
+    g, h = L.g16.double(), L.h16.double()
+    for rows, s in ((slice(N - 64, N), sign), (slice(0, 64), -torch.ones_like(sign))):
+        want = sum(((x * h[i]) @ s[i].T) * g[i, rows] for i in range(k))
+        size = sum((x.abs() @ h[i].abs())[:, None] * g[i, rows].abs() for i in range(k))
+        tol = ((k + 1) * 2.0 ** -11 + (K / 16 + 16) * 2.0 ** -23) * size + \
+            k * 2.0 ** -21 * g[:, rows].amax(0) * x.abs().sum(1, keepdim=True)
+        assert bool(((first[:, rows].double() - want).abs() <= tol + 2.0 ** -8 * want.abs()).all())
+    torch.cuda.empty_cache()
