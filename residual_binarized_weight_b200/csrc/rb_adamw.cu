@@ -22,10 +22,10 @@
 // lane as two groups of four (16-byte loads and stores of fp32, 8-byte of
 // bf16, 4-byte of codes), so a block's maximum is one warp reduction.  With fp32
 // states that runs at the copy rate.  With 8-bit states instruction issue bounds it
-// (two codes each way, the hash, a root): products and sums go two at a time (131.5
-// -> 126 us for 45 M elements, in a graph; 112 at the copy rate), and it wants warps: five
-// CTAs of 48 registers per SM 126 us, six of 40 the same (but 6.0 us against 5.1 for
-// 120 small tensors), seven and eight of 32 142 us.
+// (two codes each way, the hash, a root): 127 us for 45 M elements in a graph, 112 at the copy
+// rate.  Products and sums go two at a time (5 us less), and it wants warps: five CTAs of 48
+// registers per SM are as fast as six of 40 (but 5.1 us against 6.0 for 120 small tensors),
+// seven and eight of 32 take 16 us longer.
 #include "rbw_internal.cuh"
 
 #include <algorithm>

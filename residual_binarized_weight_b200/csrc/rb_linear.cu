@@ -24,14 +24,15 @@
 //   warp 16     issues the MMAs.
 //   warp 17     loads sign words (one thread, bulk copies, 4 KB per plane and slice) and
 //               lays out the slice's h as pairs of columns (j, j + 16).  The expansion
-//               then need not wait for the pre-pass, which prepared the pairs before
-//               (4096 x 4096, k = 2, 8 tokens: 11.2 -> 10.7 us; 5003 x 4128, k = 3, 64 tokens:
-//               19.4 -> 18.8; 11008 x 4096, k = 2, 777 tokens: 75.6 -> 74.5, in a graph).  It
+//               then need not wait for the pre-pass, which prepared the pairs before (0.5 us
+//               of 11.2 for 4096 x 4096, k = 2, 8 tokens; 0.6 of 19.4 for 5003 x 4128, k = 3, 64 tokens;
+//               1.1 of 75.6 for 11008 x 4096, k = 2, 777 tokens, in a graph).  It
 //               shares a scheduler with expansion warps, so it is kept short: the range
 //               is looked at once, on the largest |h|.
 //   warp 18     one thread loads X tiles (TMA, 128-byte swizzle), prepared by a pre-pass.
 // A pre-pass converts X to fp16, each row at a power of two of its own (rb_linear.cuh), which the
-// accumulators take back, and each 32-column group interleaved so that columns (j, j + 16) are
+// accumulators take back (0.1 us of 19.0 for 11008 x 4096, 8 tokens, 0.8 of 19.3 for 4096 x 11008, 64 tokens,
+// against one conversion for all rows), and each 32-column group interleaved so that columns (j, j + 16) are
 // neighbours: then one shift brings the sign bits of a pair to the sign bits of an fp16x2.
 //
 // Three rings: X (shared memory, up to 8 k-blocks), sign words and h pairs (by slice), and A (tensor memory, 8
@@ -594,8 +595,12 @@ struct LinPlan {
 // with a k-block's MMAs (2 cycles per token) or its expansion, whichever is longer, and a start and an
 // epilogue that nothing overlaps.  `slots` clusters of ks CTAs are resident (a cluster stays within a GPC).
 // There: see dense_plan.  Measured against each other, this / that in us: 4096 x 4096, k = 2,
-// M = 1024: 35.3 / 46.6, M = 2048: 65.8 / 72.7, M = 2560: 89.9 / 78.2; k = 4, M = 1536: 67.7 / 58.9;
-// 14336 x 4096, M = 1536: 157 / 159, M = 2048: 215 / 196; 4096 x 11008, M = 2048: 146 / 188.
+// M = 1024: 30.8 / 39.7, M = 2048: 57.3 / 66.2, M = 2560: 82.1 / 72.5; k = 4, M = 1536: 64.2 / 57.2;
+// 14336 x 4096, M = 1536: 141 / 152, M = 2048: 203 / 187; 4096 x 11008, M = 2048: 145 / 182.
+// Below 768 tokens the model favours the other form too early and is not asked: 4096 x 4096, k = 4,
+// M = 384: 29.9 / 33.0, M = 512: 30.5 / 33.3; 14336 x 4096, k = 4, M = 752: 102 / 121; 4096 x 14336, k = 4, M = 450:
+// 86.7 / 108; 8192 x 1024, k = 2, M = 640: 22.7 / 27.3; 20000 x 160, k = 2, M = 512: 26.4 / 27.7.  That costs
+// where k is large: 4096 x 4096, k = 6, M = 512: 41.0 / 40.3, k = 8, M = 384: 50.9 / 44.0, M = 752: 53.0 / 49.4.
 LinPlan plan(int N, int K, int kp, int M)
 {
     const int nkb = (K + kBK - 1) / kBK, nt = (N + kBR - 1) / kBR;
@@ -626,7 +631,7 @@ LinPlan plan(int N, int K, int kp, int M)
             }
         }
     }
-    best.dense = best.bt == 0 || (M >= 768 && dense_plan(N, K, M).cost < cost);     // (never below 1000 tokens at any size tried)
+    best.dense = best.bt == 0 || (M >= 768 && dense_plan(N, K, M).cost < cost);
     return best;
 }
 
@@ -770,7 +775,7 @@ bool outputs_meet(const LinEp& ep, int64_t M, int64_t N, std::initializer_list<B
     return false;
 }
 
-// One token goes through the byte tables (4096 x 4096, k = 2: 5.9 us against 10.5 us on the tensor cores, and exact).
+// One token goes through the byte tables (4096 x 4096, k = 2: 5.8 us against 10.6 us on the tensor cores, and exact).
 bool one_token(int k_planes, int M) { return M == 1 && k_planes <= 4; }
 
 bool good_shape(int n_out, int k_in, int k_planes, int M)

@@ -670,8 +670,11 @@ class AdamWTensor:
 
     def __setattr__(self, name, value):
         AdamWTensor._edits += 1
-        self.__dict__["edits"] = self.__dict__.get("edits", 0) + 1
-        self.__dict__[name] = value
+        d = self.__dict__
+        d["edits"] = d.get("edits", 0) + 1
+        if name not in ("grad", "lr", "weight_decay"):      # what a step may well replace each time
+            d["made"] = d["edits"]
+        d[name] = value
 
     @property
     def state_bits(self):
@@ -681,22 +684,27 @@ class AdamWTensor:
     def device(self):
         return self.param.get_device()
 
+    def _fits(self, name, types, want):
+        t, p = self.__dict__[name], self.param
+        if t is None or t.dtype not in types or t.numel() != want or not t.is_contiguous():
+            raise ValueError("%s: expected %d contiguous elements of %s" % (name, want, " or ".join(map(str, types))))
+        if t.get_device() != p.get_device():
+            raise ValueError("a parameter, its gradient and its states are on one device")
+        if name[-5:] != "scale" and t.dim() > 1 and p.dim() > 1 and t.shape != p.shape:
+            raise ValueError("%s: expected the parameter's shape, or one dimension" % name)
+
+    def check_grad(self):
+        self._fits("grad", _Y_TYPES, self.param.numel())
+
     def check(self):
-        n = self.param.numel()
-        state = torch.float32 if self.state_bits == 32 else torch.float8_e4m3fn
-        tensors = [("param", (torch.float32, torch.bfloat16), n), ("grad", (torch.float32, torch.bfloat16), n),
-                   ("exp_avg", (state,), n), ("exp_avg_sq", (state,), n)]
-        if self.state_bits == 8:
-            blocks = (n + ADAMW_BLOCK - 1) // ADAMW_BLOCK
-            tensors += [("exp_avg_scale", (torch.float32,), blocks), ("exp_avg_sq_scale", (torch.float32,), blocks)]
-        for name, types, want in tensors:
-            t = getattr(self, name)
-            if t is None or t.dtype not in types or t.numel() != want or not t.is_contiguous():
-                raise ValueError("%s: expected %d contiguous elements of %s" % (name, want, " or ".join(map(str, types))))
-            if want == n and t.dim() > 1 and self.param.dim() > 1 and t.shape != self.param.shape:
-                raise ValueError("%s: expected the parameter's shape, or one dimension" % name)
-            if t.get_device() != self.device:
-                raise ValueError("a parameter, its gradient and its states are on one device")
+        n, bits = self.param.numel(), self.state_bits
+        self._fits("param", _Y_TYPES, n)
+        self.check_grad()
+        for name in ("exp_avg", "exp_avg_sq"):
+            self._fits(name, (torch.float32 if bits == 32 else torch.float8_e4m3fn,), n)
+        if bits == 8:
+            for name in ("exp_avg_scale", "exp_avg_sq_scale"):
+                self._fits(name, (torch.float32,), (n + ADAMW_BLOCK - 1) // ADAMW_BLOCK)
 
     @staticmethod
     def new_state(param, bits=32):
@@ -732,7 +740,7 @@ class AdamW:
 
     def refresh(self):
         self._table = (RbAdamWTensor * len(self.tensors))()
-        self._taken = [-1] * len(self.tensors)              # each tensor's count of assignments when its row was made
+        self._taken = [(-1, -1)] * len(self.tensors)        # each tensor's counts of assignments when its row was made
         self._follow()
 
     def _follow(self):
@@ -740,10 +748,18 @@ class AdamW:
             raise ValueError("expected tensors of one device, at least one")
         edits = AdamWTensor._edits
         for i, t in enumerate(self.tensors):
-            if t.edits != self._taken[i]:
+            now, taken = (t.made, t.edits), self._taken[i]
+            if now == taken:
+                continue
+            if t.made == taken[0]:                          # the gradient, the rate or the decay
+                t.check_grad()
+                row = self._table[i]
+                row.grad, row.grad_dtype = t.grad.data_ptr(), RB_BF16 if t.grad.dtype == torch.bfloat16 else RB_F32
+                row.lr, row.weight_decay = t.lr, t.weight_decay
+            else:
                 t.check()
                 self._table[i] = t.struct()
-                self._taken[i] = t.edits
+            self._taken[i] = now
         self._edits = edits
 
     def step(self, step, lr_scale=None, grad_scale=None, dev_status=None, flags=0, stream=None):

@@ -32,10 +32,15 @@ def test_the_optimizer_follows_what_is_assigned():
     row = opt._table[1]
     assert row.grad == new.data_ptr() and row.lr == 0.5 and row.weight_decay == 0.25
     assert opt._table[0].grad == old[0] and opt._table[2].grad == old[2]
+    ts[0].grad = torch.zeros(300, dtype=torch.bfloat16)
+    opt._follow()
+    assert (opt._table[0].grad, opt._table[0].grad_dtype) == (ts[0].grad.data_ptr(), rbw.RB_BF16)
+    assert opt._table[0].exp_avg == ts[0].exp_avg.data_ptr()
     ts[2].exp_avg = torch.zeros(300)
     other = rbw.AdamW(ts)                                                            # a second list over the same tensors
     opt._follow()
     assert opt._table[2].exp_avg == other._table[2].exp_avg == ts[2].exp_avg.data_ptr()
+    assert [bytes(x) for x in opt._table] == [bytes(x) for x in other._table]
 
 
 @pytest.mark.parametrize("name,value", [
