@@ -515,8 +515,9 @@ typedef struct {
  *   ep   nullable: Y = P = X What^T.
  *   Y    [M][N] fp32 or bf16, row stride ldy.
  * Y and preact must not overlap each other, an input (the layer's arrays among them) or the
- * workspace, except Y = residual as above (RB_ERR_ARG).  Arrays of one row stride in bytes may share rows side by side (the halves
- * of a [M][2N] buffer); with different strides, address ranges that meet are refused.
+ * workspace, except Y = residual as above (RB_ERR_ARG).  Arrays of one row stride in bytes may
+ * share rows side by side (the halves of a [M][2N] buffer); with different strides, address
+ * ranges that meet are refused.
  *   workspace  rb_linear_workspace_bytes(N, K, k, M) bytes (X in fp16 and a factor per row; where
  *              the weights are expanded once for some thousand tokens, 2 N K bytes more);
  *              no clearing needed; calls that share one must not overlap on the GPU.

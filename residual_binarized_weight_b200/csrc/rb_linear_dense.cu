@@ -5,7 +5,8 @@
 // (rb_linear.cu); from some hundred tokens on it is cheaper to write the expanded
 // matrix once, 2 bytes per weight, and let TMA bring both operands.
 //
-// Pass 1 (expand_kernel): X16 = fp16(X), rows at powers of two of their own (rb_linear.cuh), and W16[n][c] = fp16(sum_i (g_i[n] 2^-e) (B_i h_i[c])),
+// Pass 1 (expand_kernel): X16 = fp16(X), each row at a power of two of its own (rb_linear.cuh),
+// and W16[n][c] = fp16(sum_i (g_i[n] 2^-e) (B_i h_i[c])),
 // scale[n] = 2^e with k max_i |g_i| <= 2^e, so that no sum overflows and the
 // ratios of fp16 scales are exact; k = 1: W16 = +-h, scale = g, exact.  Both
 // matrices hold each 32-column group in the order 0, 16, 1, 17, ..: the signs of
